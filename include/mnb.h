@@ -355,6 +355,118 @@ MNB_API int mnb_gptq_quantize(const float *W, const float *U, const uint8_t *dea
                               int has_zp, uint8_t *packed, void *scales, mnb_dtype scale_t, uint8_t *zp,
                               void *stream);
 
+/* ---- the paged key-value cache of a decode step ---------------------------
+ * Between the q|k|v projections of a decoder layer and its o projection stands
+ * the attention over the keys and values of all earlier tokens ("Qwen3-ASR-0.6B
+ * -- ONNX for the browser", "Graph contracts": past_key_values of 8 heads of
+ * 128, kept on the GPU from step to step; "qwen3-asr-0.6b-onnx-int4-merged":
+ * a prompt's state is reused).  Here those rows live in a pool of pages, and a
+ * request owns the pages that its row of a block table names:
+ *   token at position p of request b: page block_table[b][p / page_size],
+ *   slot = page * page_size + p % page_size.
+ * mnb_paged_tables hands out pages and computes the slots of a step's new
+ * tokens, mnb_rope_append writes their keys and values, mnb_paged_attention
+ * reads them.  All three take MNB_FLAG_PDL (they read nothing before the
+ * previous kernel has finished) and can be captured into a CUDA graph: lengths,
+ * tables and slots are read on the device at every launch.
+ *
+ * `status` of the three: NULL, or a device int into which bits are ORed (the
+ * caller clears it); whatever they report is left out of the work, nothing is
+ * read or written out of bounds for it:
+ *   bit 0  a page id, slot or position outside its range,
+ *   bit 1  a length below 0 or above its room,
+ *   bit 2  (mnb_paged_tables) the free list has run out. */
+typedef struct mnb_paged_cache {
+    void *k, *v;            /* keys and values: row of (page, offset, head) at the strides below */
+    int64_t num_pages;      /* pages in the pool; num_pages * page_size < 2^31 */
+    int64_t page_size;      /* tokens per page, any positive number */
+    int64_t num_heads;      /* KV heads */
+    int64_t head_dim;       /* entries of a head, contiguous; a multiple of 8, <= 256 */
+    int64_t page_stride, slot_stride, head_stride;   /* elements, the same for k and v; multiples of 16 bytes */
+    int32_t dtype;          /* MNB_F16 or MNB_F32: of the cache and of q, k, v and out */
+    int32_t reserved;       /* 0 */
+} mnb_paged_cache;
+
+/* Block tables, slots and positions of a step's new tokens, on the GPU.
+ * Request b holds ctx_lens[b] tokens and gets new_lens[b] more; the new tokens
+ * of all requests stand one request behind the other.  Pages of request b:
+ * blocks(n) = ceil(n / page_size) of them hold n tokens, so
+ *   need_b = blocks(ctx_b + new_b) - blocks(ctx_b)
+ * are taken from free_pages in request order, from index *free_start on, into
+ * columns blocks(ctx_b) .. of row b of block_table; other entries stay as they
+ * are.  Writes
+ *   seq_lens[b]  = ctx_b + new_b            cu_new[b] = sum_{i<b} new_i, b <= B
+ *   slots[t], positions[t]                  for every new token t
+ *   *free_next   = *free_start + pages taken
+ * and slots[t] = -1, positions[t] = 0 for sum new <= t < T (a step padded to T
+ * tokens: mnb_rope_append skips slot -1).
+ * A request is refused, takes no page, keeps seq_lens[b] = max(ctx_b, 0) and
+ * gives its tokens slot -1, when a length is negative or ctx_b + new_b exceeds
+ * max_blocks * page_size or its tokens do not fit into T (status bit 1), or
+ * when it needs pages that the list no longer has (bit 2: from that request on
+ * only requests that need no page are granted).  A page id outside
+ * [0, num_pages) gives slot -1 (bit 0).  A negative new_lens counts as 0 tokens; cu_new
+ * stops at 2^31 - 1.
+ * Outputs must not overlap inputs (block_table is both).  0 <= B <= 4096.
+ * Errors: MNB_ERR_INVALID_ARG, MNB_ERR_SHAPE, MNB_ERR_ALIGN,
+ *         MNB_ERR_UNSUPPORTED (B > 4096), MNB_ERR_CUDA. */
+MNB_API int mnb_paged_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B, int64_t page_size,
+                             int64_t num_pages, const int32_t *free_pages, int64_t num_free,
+                             const int32_t *free_start, int32_t *block_table, int64_t table_stride,
+                             int64_t max_blocks, int32_t *seq_lens, int32_t *cu_new, int32_t *slots,
+                             int32_t *positions, int64_t T, int32_t *free_next, int *status, unsigned flags,
+                             void *stream);
+
+/* The new tokens' q, k and v on their way into the attention and the cache.
+ * For each token t, with c, s = rows positions[t] of the tables cos and sin
+ * (fp32 [num_pos][rot_dim / 2]) and x a head of q or k:
+ *   x <- x * w / sqrt(mean(x^2) + eps)          when q_weight / k_weight (fp32 [D]) is given,
+ *   (x_i, x_{i+R/2}) <- (x_i c_i - x_{i+R/2} s_i, x_{i+R/2} c_i + x_i s_i),  i < R/2, R = rot_dim,
+ * all in fp32, rounded once; q goes to q_out (which may be q itself), k and v
+ * (v as it is) to slot slots[t] of the cache.  rot_dim is a multiple of 8, at
+ * most D; 0 = no rotation (positions, cos and sin are then not read).  Hq = 0:
+ * no q.  Strides are in elements, multiples of 16 bytes; q, k and v may be
+ * parts of one [T][(Hq + 2 Hkv) D] product.
+ * A token with slot -1 has its q written and its k and v dropped; so has one
+ * whose slot is out of range (status bit 0).  A position outside [0, num_pos)
+ * gives a zero q row and drops k and v (bit 0).  Two tokens must not have the
+ * same slot.
+ * Errors: MNB_ERR_INVALID_ARG, MNB_ERR_SHAPE, MNB_ERR_ALIGN, MNB_ERR_CUDA. */
+MNB_API int mnb_rope_append(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+                            int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                            int64_t v_head_stride, const mnb_paged_cache *cache, const int32_t *slots,
+                            const int32_t *positions, int64_t T, int64_t Hq, const float *cos, const float *sin,
+                            int64_t rot_dim, int64_t num_pos, const float *q_weight, const float *k_weight,
+                            float eps, void *q_out, int64_t o_token_stride, int64_t o_head_stride, int *status,
+                            unsigned flags, void *stream);
+
+/* Attention of one new token per request over its pages (decode; grouped heads:
+ * query head i reads KV head i / (Hq / Hkv)).  With n = seq_lens[b] and j < n,
+ *   s_j = scale * q[b][i] . k_j,  lse[b][i] = log sum_j exp(s_j) (natural log),
+ *   out[b][i] = sum_j exp(s_j - lse) v_j.
+ * Scores, softmax statistics and sums are fp32; with fp16, the probabilities
+ * are rounded to fp16 for their product with V.  n = 0: out = 0, lse = -inf
+ * (a batch padded to B requests).  n above max_blocks * page_size counts as
+ * that, n below 0 as 0 (status bit 1); keys of a page id outside the pool are
+ * left out (bit 0).  Nothing behind a request's n tokens is read: entries of
+ * the block table and rows of its last page there may hold anything.
+ *   lse fp32 [B][Hq] or NULL.  1 <= Hq <= 4096, Hq % Hkv == 0, 0 <= B <= 4096.
+ *   Results are the same, bit for bit, from call to call on one GPU model.
+ * workspace: mnb_paged_attention_workspace_bytes (for the current device),
+ * 16-byte aligned, ZERO-FILLED before its first use; its first bytes count
+ * arrivals and every call leaves them zero again, so it serves call after call,
+ * of any sizes that it is large enough for; calls that share one must not run
+ * at the same time on the GPU.
+ * Errors: MNB_ERR_INVALID_ARG (also: workspace too small), MNB_ERR_SHAPE,
+ *         MNB_ERR_ALIGN, MNB_ERR_UNSUPPORTED, MNB_ERR_CUDA. */
+MNB_API size_t mnb_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                                   mnb_dtype dtype);   /* 0 for sizes the call refuses */
+MNB_API int mnb_paged_attention(const void *q, int64_t q_request_stride, int64_t q_head_stride,
+                                const mnb_paged_cache *cache, const int32_t *block_table, int64_t table_stride,
+                                int64_t max_blocks, const int32_t *seq_lens, int64_t B, int64_t Hq, float scale,
+                                void *out, int64_t o_request_stride, int64_t o_head_stride, float *lse,
+                                void *workspace, size_t ws_bytes, int *status, unsigned flags, void *stream);
+
 /* Reads (and, if clear != 0, zeroes) the library's device status word on the
  * current device into *status_out: bit 0 = a GEMM or GEMV mbarrier wait timed
  * out; bits 1-3 = mnb_gemv_chain (see there).  Synchronizes the device.

@@ -25,7 +25,8 @@ __all__ = [
     "mnb_gemv_argmax", "mnb_gemv_argmax_workspace_bytes", "mnb_gemv_argmax_noalloc", "mnb_gemv_swiglu",
     "mnb_gemv_task", "mnb_gemv_chain_plan_bytes", "mnb_gemv_chain_workspace_bytes", "mnb_gemv_chain_plan",
     "mnb_gemv_chain", "mnb_matmul", "mnb_gptq_hessian", "mnb_gptq_workspace_bytes", "mnb_gptq_prepare",
-    "mnb_gptq_quantize",
+    "mnb_gptq_quantize", "mnb_paged_cache", "mnb_paged_tables", "mnb_rope_append", "mnb_paged_attention",
+    "mnb_paged_attention_workspace_bytes",
 ]
 
 MNB_F32, MNB_F16 = 0, 1
@@ -48,6 +49,14 @@ class mnb_gemv_task(ctypes.Structure):
     _fields_ = [("X", ctypes.c_void_p), ("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("zp", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("wait", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class mnb_paged_cache(ctypes.Structure):
+    """The pool of a paged key-value cache (the C struct of the same name)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("num_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def _load():
@@ -82,6 +91,13 @@ def _load():
         "mnb_gptq_workspace_bytes": ([i64], sz),
         "mnb_gptq_prepare": ([vp, i64, ctypes.c_float, vp, vp, vp, sz, P(ctypes.c_float), vp], i32),
         "mnb_gptq_quantize": ([vp, vp, vp, i64, i64, i32, i32, vp, vp, i32, vp, vp], i32),
+        "mnb_paged_tables": ([vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, i64, vp, vp, u32, vp],
+                             i32),
+        "mnb_rope_append": ([vp, i64, i64, vp, i64, i64, vp, i64, i64, P(mnb_paged_cache), vp, vp, i64, i64, vp, vp,
+                             i64, i64, vp, vp, ctypes.c_float, vp, i64, i64, vp, u32, vp], i32),
+        "mnb_paged_attention_workspace_bytes": ([i64, i64, i64, i64, i32], sz),
+        "mnb_paged_attention": ([vp, i64, i64, P(mnb_paged_cache), vp, i64, i64, vp, i64, i64, ctypes.c_float, vp,
+                                 i64, i64, vp, vp, sz, vp, u32, vp], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -296,3 +312,153 @@ def mnb_gptq_quantize(W, U, dead, bs, has_zp, packed, scales, zp, stream=None):
         _ptr(W), _ptr(U), _ptr(dead), N, K, bs, int(bool(has_zp)), _ptr(packed), _ptr(scales), _dt(scales),
         _ptr(zp), _stream(stream)))
 
+
+
+def _device_tensors(fn, dtype, **ts):
+    """Each given tensor (None passes) is of `dtype` (None: any) and on the current CUDA device."""
+    for name, t in ts.items():
+        if t is None:
+            continue
+        if dtype is not None and t.dtype != dtype:
+            raise MnbError(fn, -1, f"{name} is {t.dtype}, not {dtype}")
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise MnbError(fn, -1, f"{name} is on {t.device}, not on the current CUDA device")
+
+
+def _shaped(fn, name, t, *shape):
+    if tuple(t.shape) != shape:
+        raise MnbError(fn, -2, f"{name} has shape {tuple(t.shape)}, not {shape}")
+
+
+def _vectors(fn, n, **ts):
+    for name, t in ts.items():
+        if t is not None:
+            _shaped(fn, name, t, n)
+            if not t.is_contiguous():
+                raise MnbError(fn, -1, f"{name} must be contiguous")
+
+
+def _status_word(fn, status):
+    _device_tensors(fn, torch.int32, status=status)
+    if status is not None and status.numel() != 1:
+        raise MnbError(fn, -2, "status must have one element")
+
+
+def _rows(fn, name, t, n, heads, D):
+    """(pointer, row stride, head stride) of t [n, heads, D] with contiguous heads."""
+    if t is None:
+        return None, 0, 0
+    _shaped(fn, name, t, n, heads, D)
+    if D > 1 and t.stride(2) != 1:
+        raise MnbError(fn, -1, f"{name}'s last dimension must be contiguous")
+    return _ptr(t), t.stride(0) if n > 1 else 0, t.stride(1) if heads > 1 else 0
+
+
+def _paged_cache(fn, k_cache, v_cache):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise MnbError(fn, -2, "k_cache and v_cache must have one shape [pages, page_size, heads, head size]")
+    if v_cache.dtype != k_cache.dtype or k_cache.dtype not in (torch.float16, torch.float32):
+        raise MnbError(fn, -1, f"k_cache is {k_cache.dtype}, v_cache {v_cache.dtype}: fp16 or fp32, the same")
+    _device_tensors(fn, k_cache.dtype, k_cache=k_cache, v_cache=v_cache)
+    P, ps, H, D = k_cache.shape
+    strides = [st if n > 1 else 0 for st, n in zip(k_cache.stride(), k_cache.shape)]
+    if strides != [st if n > 1 else 0 for st, n in zip(v_cache.stride(), v_cache.shape)] or (D > 1 and strides[3] != 1):
+        raise MnbError(fn, -1, "k_cache and v_cache must have the same strides, the last dimension contiguous")
+    return mnb_paged_cache(_ptr(k_cache), _ptr(v_cache), P, ps, H, D, strides[0], strides[1], strides[2],
+                           _dt(k_cache), 0)
+
+
+def _block_table(fn, block_table, B):
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise MnbError(fn, -2, f"block_table has shape {tuple(block_table.shape)}, not [{B}, blocks]")
+    if B > 0 and block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise MnbError(fn, -1, "block_table's rows must be contiguous")
+    return block_table.stride(0) if B > 1 else block_table.shape[1]
+
+
+def mnb_paged_tables(ctx_lens, new_lens, block_table, page_size, num_pages, free_pages, free_start, seq_lens, cu_new,
+                     slots, positions, free_next, status=None, flags=0, stream=None):
+    """Pages for new_lens [B] more tokens behind ctx_lens [B]: taken from free_pages [F], at free_start [1] and on,
+    into block_table [B, blocks]; seq_lens [B], cu_new [B + 1], slots and positions [T] of the new tokens (-1 and 0
+    behind the last), free_next [1].  All int32."""
+    fn = "mnb_paged_tables"
+    _device_tensors(fn, torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table,
+                    free_pages=free_pages, free_start=free_start, seq_lens=seq_lens, cu_new=cu_new, slots=slots,
+                    positions=positions, free_next=free_next)
+    _status_word(fn, status)
+    B, T = ctx_lens.numel(), slots.numel()
+    _vectors(fn, B, ctx_lens=ctx_lens, new_lens=new_lens, seq_lens=seq_lens)
+    _vectors(fn, B + 1, cu_new=cu_new)
+    _vectors(fn, T, slots=slots, positions=positions)
+    _vectors(fn, 1, free_start=free_start, free_next=free_next)
+    _vectors(fn, free_pages.numel(), free_pages=free_pages)
+    stride = _block_table(fn, block_table, B)
+    _check(fn, _lib.mnb_paged_tables(
+        _ptr(ctx_lens), _ptr(new_lens), B, page_size, num_pages, _ptr(free_pages), free_pages.numel(),
+        _ptr(free_start), _ptr(block_table), stride, block_table.shape[1], _ptr(seq_lens), _ptr(cu_new), _ptr(slots),
+        _ptr(positions), T, _ptr(free_next), _ptr(status), flags, _stream(stream)))
+
+
+def mnb_rope_append(q, k, v, k_cache, v_cache, slots, positions, cos, sin, q_out, q_weight=None, k_weight=None,
+                    eps=1e-6, status=None, flags=0, stream=None):
+    """RMS norm (where a weight [D] is given) and rotary embedding (unless cos is None) of q [T, Hq, D] into q_out and
+    of k [T, Hkv, D] into rows slots [T] of k_cache [pages, page_size, Hkv, D]; v likewise, as it is, into v_cache.
+    cos, sin: fp32 [positions, rot_dim / 2].  q and q_out may be None (keys and values alone), or one tensor."""
+    fn = "mnb_rope_append"
+    if (q is None) != (q_out is None):
+        raise MnbError(fn, -1, "q and q_out go together")
+    if (cos is None) != (sin is None):
+        raise MnbError(fn, -1, "cos and sin go together")
+    if cos is not None and positions is None:
+        raise MnbError(fn, -1, "a rotation needs positions")
+    cache = _paged_cache(fn, k_cache, v_cache)
+    H, D = k_cache.shape[2:]
+    T, Hq = slots.numel(), 0 if q is None else q.shape[1] if q.dim() == 3 else -1
+    _device_tensors(fn, k_cache.dtype, q=q, k=k, v=v, q_out=q_out)
+    _device_tensors(fn, torch.float32, cos=cos, sin=sin, q_weight=q_weight, k_weight=k_weight)
+    _device_tensors(fn, torch.int32, slots=slots, positions=positions)
+    _status_word(fn, status)
+    _vectors(fn, T, slots=slots, positions=positions)
+    _vectors(fn, D, q_weight=q_weight, k_weight=k_weight)
+    R = num_pos = 0
+    if cos is not None:
+        if cos.dim() != 2 or sin.shape != cos.shape:
+            raise MnbError(fn, -2, "cos and sin must have one shape [positions, rot_dim / 2]")
+        _contiguous(fn, cos, sin)
+        num_pos, R = cos.shape[0], 2 * cos.shape[1]
+    _check(fn, _lib.mnb_rope_append(
+        *_rows(fn, "q", q, T, Hq, D), *_rows(fn, "k", k, T, H, D), *_rows(fn, "v", v, T, H, D), ctypes.byref(cache),
+        _ptr(slots), _ptr(positions), T, Hq, _ptr(cos), _ptr(sin), R, num_pos, _ptr(q_weight), _ptr(k_weight), eps,
+        *_rows(fn, "q_out", q_out, T, Hq, D), _ptr(status), flags, _stream(stream)))
+
+
+def mnb_paged_attention_workspace_bytes(B, Hq, Hkv, D, dtype=torch.float16) -> int:
+    """Bytes of (zero-filled) workspace of mnb_paged_attention on the current device."""
+    return _lib.mnb_paged_attention_workspace_bytes(B, Hq, Hkv, D, MNB_F16 if dtype == torch.float16 else MNB_F32)
+
+
+def mnb_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, workspace, lse=None, status=None,
+                        flags=0, stream=None):
+    """out [B, Hq, D] = softmax(scale * q k^T) v of one token per request over the first seq_lens [B] rows of its
+    pages block_table [B, blocks] of k_cache, v_cache [pages, page_size, Hkv, D]; lse fp32 [B, Hq].
+    workspace: a zero-filled uint8 tensor of mnb_paged_attention_workspace_bytes bytes."""
+    fn = "mnb_paged_attention"
+    cache = _paged_cache(fn, k_cache, v_cache)
+    D = k_cache.shape[3]
+    if q.dim() != 3:
+        raise MnbError(fn, -2, f"q has shape {tuple(q.shape)}, not [requests, heads, head size]")
+    B, Hq = q.shape[:2]
+    _device_tensors(fn, k_cache.dtype, q=q, out=out)
+    _device_tensors(fn, torch.int32, block_table=block_table, seq_lens=seq_lens)
+    _device_tensors(fn, torch.float32, lse=lse)
+    _device_tensors(fn, None, workspace=workspace)
+    _status_word(fn, status)
+    _vectors(fn, B, seq_lens=seq_lens)
+    if lse is not None:
+        _shaped(fn, "lse", lse, B, Hq)
+    _contiguous(fn, lse, workspace)
+    stride = _block_table(fn, block_table, B)
+    _check(fn, _lib.mnb_paged_attention(
+        *_rows(fn, "q", q, B, Hq, D), ctypes.byref(cache), _ptr(block_table), stride, block_table.shape[1],
+        _ptr(seq_lens), B, Hq, scale, *_rows(fn, "out", out, B, Hq, D), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(status), flags, _stream(stream)))

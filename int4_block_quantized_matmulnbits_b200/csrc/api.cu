@@ -4,6 +4,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "common.cuh"
@@ -115,6 +116,41 @@ static int check_matmul_args(const char *fn, const void *X, int act_t, const uin
         return fail(MNB_ERR_ALIGN, "%s: X, packed and Y must be 16-byte aligned", fn);
     if (!aligned(scales, scale_t == MNB_F32 ? 4 : 2))
         return fail(MNB_ERR_ALIGN, "%s: scales misaligned", fn);
+    return MNB_OK;
+}
+
+// Limits of the paged cache: slots are int32, the request scans are one CTA's,
+// and page * stride stays far below 2^63.
+static const int64_t kMaxSlots = ((int64_t)1 << 31) - 1, kMaxRequests = 4096, kMaxHeads = 4096;
+static const int64_t kMaxStride = (int64_t)1 << 31;
+
+static int check_stride(const char *fn, int64_t stride, int dtype) {
+    const int64_t unit = dtype == MNB_F16 ? 8 : 4;
+    if (stride < 0 || stride > kMaxStride)
+        return fail(MNB_ERR_SHAPE, "%s: stride %lld outside [0, 2^31]", fn, (long long)stride);
+    if (stride % unit)
+        return fail(MNB_ERR_ALIGN, "%s: stride %lld is not a multiple of 16 bytes", fn, (long long)stride);
+    return MNB_OK;
+}
+
+static int check_paged_cache(const char *fn, const mnb_paged_cache *c) {
+    int rc;
+    if (!c || !c->k || !c->v)
+        return fail(MNB_ERR_INVALID_ARG, "%s: NULL cache", fn);
+    if ((rc = check_dtype(fn, "cache", c->dtype)))
+        return rc;
+    if (c->page_size < 1 || c->num_pages < 1 || c->page_size > kMaxSlots || c->num_pages > kMaxSlots / c->page_size)
+        return fail(MNB_ERR_SHAPE, "%s: %lld pages of %lld tokens (at least one, below 2^31 tokens)", fn,
+                    (long long)c->num_pages, (long long)c->page_size);
+    if (c->num_heads < 1 || c->num_heads > kMaxHeads)
+        return fail(MNB_ERR_SHAPE, "%s: %lld KV heads", fn, (long long)c->num_heads);
+    if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8)
+        return fail(MNB_ERR_SHAPE, "%s: head size %lld is not a multiple of 8 up to 256", fn, (long long)c->head_dim);
+    if (!aligned(c->k, 16) || !aligned(c->v, 16))
+        return fail(MNB_ERR_ALIGN, "%s: the cache must be 16-byte aligned", fn);
+    for (int64_t st : {c->page_stride, c->slot_stride, c->head_stride})
+        if ((rc = check_stride(fn, st, c->dtype)))
+            return rc;
     return MNB_OK;
 }
 
@@ -460,6 +496,148 @@ int mnb_gptq_quantize(const float *W, const float *U, const uint8_t *dead, int64
         return fail(MNB_ERR_ALIGN, "%s: W, U and scales need their element alignment", fn);
     return launch_gptq_quantize(W, U, dead, N, K, bs, has_zp ? 1 : 0, packed, scales, scale_t == MNB_F16,
                                 has_zp ? zp : nullptr, (cudaStream_t)stream);
+}
+
+int mnb_paged_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B, int64_t page_size,
+                     int64_t num_pages, const int32_t *free_pages, int64_t num_free, const int32_t *free_start,
+                     int32_t *block_table, int64_t table_stride, int64_t max_blocks, int32_t *seq_lens,
+                     int32_t *cu_new, int32_t *slots, int32_t *positions, int64_t T, int32_t *free_next, int *status,
+                     unsigned flags, void *stream) {
+    clear_error();
+    const char *fn = "mnb_paged_tables";
+    if (B < 0 || T < 0 || num_free < 0)
+        return fail(MNB_ERR_INVALID_ARG, "%s: negative size (B=%lld T=%lld num_free=%lld)", fn, (long long)B,
+                    (long long)T, (long long)num_free);
+    if (B > kMaxRequests)
+        return fail(MNB_ERR_UNSUPPORTED, "%s: B=%lld above %lld", fn, (long long)B, (long long)kMaxRequests);
+    if (page_size < 1 || num_pages < 1 || page_size > kMaxSlots || num_pages > kMaxSlots / page_size)
+        return fail(MNB_ERR_SHAPE, "%s: %lld pages of %lld tokens (at least one, below 2^31 tokens)", fn,
+                    (long long)num_pages, (long long)page_size);
+    if (max_blocks < 1 || max_blocks > kMaxSlots / page_size || table_stride < max_blocks || table_stride > kMaxStride)
+        return fail(MNB_ERR_SHAPE, "%s: block table of %lld columns, row stride %lld", fn, (long long)max_blocks,
+                    (long long)table_stride);
+    if (T > kMaxDim || num_free > kMaxDim)
+        return fail(MNB_ERR_SHAPE, "%s: T or num_free above 2^30", fn);
+    if (flags & ~(unsigned)MNB_FLAG_PDL)
+        return fail(MNB_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
+    if ((B > 0 && (!ctx_lens || !new_lens || !block_table || !seq_lens)) || (num_free > 0 && !free_pages) ||
+        (T > 0 && (!slots || !positions)) || !free_start || !free_next || !cu_new)
+        return fail(MNB_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    for (const void *ptr : {(const void *)ctx_lens, (const void *)new_lens, (const void *)free_pages,
+                            (const void *)free_start, (const void *)block_table, (const void *)seq_lens,
+                            (const void *)cu_new, (const void *)slots, (const void *)positions,
+                            (const void *)free_next, (const void *)status})
+        if (!aligned(ptr, 4))
+            return fail(MNB_ERR_ALIGN, "%s: a pointer is not 4-byte aligned", fn);
+    if (free_next == free_start || (B > 0 && (seq_lens == ctx_lens || seq_lens == new_lens)))
+        return fail(MNB_ERR_INVALID_ARG, "%s: an output is an input's buffer", fn);
+    return launch_paged_tables(ctx_lens, new_lens, (int)B, (int)page_size, (int)num_pages, free_pages, (int)num_free,
+                               free_start, block_table, table_stride, (int)max_blocks, seq_lens, cu_new, slots,
+                               positions, (int)T, free_next, status, flags, (cudaStream_t)stream);
+}
+
+int mnb_rope_append(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs,
+                    const void *v, int64_t v_ts, int64_t v_hs, const mnb_paged_cache *cache, const int32_t *slots,
+                    const int32_t *positions, int64_t T, int64_t Hq, const float *cos, const float *sin,
+                    int64_t rot_dim, int64_t num_pos, const float *q_weight, const float *k_weight, float eps,
+                    void *q_out, int64_t o_ts, int64_t o_hs, int *status, unsigned flags, void *stream) {
+    clear_error();
+    const char *fn = "mnb_rope_append";
+    int rc = check_paged_cache(fn, cache);
+    if (rc)
+        return rc;
+    if (T < 0 || Hq < 0 || rot_dim < 0)
+        return fail(MNB_ERR_INVALID_ARG, "%s: negative size (T=%lld Hq=%lld rot_dim=%lld)", fn, (long long)T,
+                    (long long)Hq, (long long)rot_dim);
+    if (T > kMaxDim || Hq > kMaxHeads)
+        return fail(MNB_ERR_SHAPE, "%s: T above 2^30 or Hq above %lld", fn, (long long)kMaxHeads);
+    if (rot_dim % 8 || rot_dim > cache->head_dim)
+        return fail(MNB_ERR_SHAPE, "%s: rot_dim=%lld is not a multiple of 8 up to D=%lld", fn, (long long)rot_dim,
+                    (long long)cache->head_dim);
+    if (rot_dim && (num_pos < 1 || num_pos > kMaxSlots))
+        return fail(MNB_ERR_SHAPE, "%s: num_pos=%lld", fn, (long long)num_pos);
+    if (!(eps >= 0.0f) || !(eps <= 3.0e38f))
+        return fail(MNB_ERR_INVALID_ARG, "%s: eps is negative or not finite", fn);
+    if (flags & ~(unsigned)MNB_FLAG_PDL)
+        return fail(MNB_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
+    if (T == 0)
+        return MNB_OK;
+    if (!k || !v || !slots || (Hq && (!q || !q_out)) || (rot_dim && (!positions || !cos || !sin)))
+        return fail(MNB_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    for (const void *ptr : {q, k, v, (const void *)q_out, (const void *)cos, (const void *)sin, (const void *)q_weight,
+                            (const void *)k_weight})
+        if (!aligned(ptr, 16))
+            return fail(MNB_ERR_ALIGN, "%s: a pointer is not 16-byte aligned", fn);
+    if (!aligned(slots, 4) || !aligned(positions, 4) || !aligned(status, 4))
+        return fail(MNB_ERR_ALIGN, "%s: slots, positions and status need 4-byte alignment", fn);
+    for (int64_t st : {q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs})
+        if ((rc = check_stride(fn, st, cache->dtype)))
+            return rc;
+    // rows that are written must not lie on one another
+    const int64_t D = cache->head_dim;
+    if ((cache->num_heads > 1 && cache->head_stride < D) || (cache->page_size > 1 && cache->slot_stride < D) ||
+        (cache->num_pages > 1 && cache->page_stride < D) || (Hq > 1 && o_hs < D) || (Hq && T > 1 && o_ts < D))
+        return fail(MNB_ERR_SHAPE, "%s: rows of the cache or of q_out overlap", fn);
+    if (Hq && q_out == q && ((T > 1 && o_ts != q_ts) || (Hq > 1 && o_hs != q_hs)))
+        return fail(MNB_ERR_INVALID_ARG, "%s: q_out is q with other strides", fn);
+    return launch_rope_append(q, q_ts, q_hs, k, k_ts, k_hs, v, v_ts, v_hs, cache, slots, positions, T, (int)Hq, cos,
+                              sin, (int)rot_dim, (int)num_pos, q_weight, k_weight, eps, q_out, o_ts, o_hs, status,
+                              flags, (cudaStream_t)stream);
+}
+
+size_t mnb_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, mnb_dtype dtype) {
+    if (B < 0 || B > kMaxRequests || Hkv < 1 || Hq < Hkv || Hq > kMaxHeads || Hq % Hkv || D < 8 || D > 256 || D % 8 ||
+        (dtype != MNB_F16 && dtype != MNB_F32))
+        return 0;
+    return paged_attention_workspace_bytes((int)Hq, (int)Hkv, (int)D, dtype == MNB_F16);
+}
+
+int mnb_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_paged_cache *cache,
+                        const int32_t *block_table, int64_t table_stride, int64_t max_blocks, const int32_t *seq_lens,
+                        int64_t B, int64_t Hq, float scale, void *out, int64_t o_bs, int64_t o_hs, float *lse,
+                        void *workspace, size_t ws_bytes, int *status, unsigned flags, void *stream) {
+    clear_error();
+    const char *fn = "mnb_paged_attention";
+    int rc = check_paged_cache(fn, cache);
+    if (rc)
+        return rc;
+    if (B < 0 || Hq < 1)
+        return fail(MNB_ERR_INVALID_ARG, "%s: B=%lld Hq=%lld", fn, (long long)B, (long long)Hq);
+    if (B > kMaxRequests)
+        return fail(MNB_ERR_UNSUPPORTED, "%s: B=%lld above %lld", fn, (long long)B, (long long)kMaxRequests);
+    if (Hq > kMaxHeads || Hq % cache->num_heads)
+        return fail(MNB_ERR_SHAPE, "%s: Hq=%lld is not a multiple of %lld KV heads up to %lld", fn, (long long)Hq,
+                    (long long)cache->num_heads, (long long)kMaxHeads);
+    if (max_blocks < 1 || max_blocks > kMaxSlots / cache->page_size || table_stride < max_blocks ||
+        table_stride > kMaxStride)
+        return fail(MNB_ERR_SHAPE, "%s: block table of %lld columns, row stride %lld", fn, (long long)max_blocks,
+                    (long long)table_stride);
+    if (B * ((max_blocks * cache->page_size + 7) / 8) > kMaxSlots)
+        return fail(MNB_ERR_SHAPE, "%s: B * max_blocks * page_size is 2^34 or more", fn);
+    if (!(scale >= -3.0e38f && scale <= 3.0e38f))
+        return fail(MNB_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+    if (flags & ~(unsigned)MNB_FLAG_PDL)
+        return fail(MNB_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
+    if (B == 0)
+        return MNB_OK;
+    if (!q || !out || !block_table || !seq_lens || !workspace)
+        return fail(MNB_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16))
+        return fail(MNB_ERR_ALIGN, "%s: q, out and workspace must be 16-byte aligned", fn);
+    if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(status, 4))
+        return fail(MNB_ERR_ALIGN, "%s: block_table, seq_lens, lse and status need 4-byte alignment", fn);
+    for (int64_t st : {q_bs, q_hs, o_bs, o_hs})
+        if ((rc = check_stride(fn, st, cache->dtype)))
+            return rc;
+    if ((Hq > 1 && o_hs < cache->head_dim) || (B > 1 && o_bs < cache->head_dim))
+        return fail(MNB_ERR_SHAPE, "%s: rows of out overlap", fn);
+    const size_t need = paged_attention_workspace_bytes((int)Hq, (int)cache->num_heads, (int)cache->head_dim,
+                                                        cache->dtype == MNB_F16);
+    if (ws_bytes < need)
+        return fail(MNB_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+    return launch_paged_attention(q, q_bs, q_hs, cache, block_table, table_stride, (int)max_blocks, seq_lens, (int)B,
+                                  (int)Hq, scale, out, o_bs, o_hs, lse, workspace, status, flags,
+                                  (cudaStream_t)stream);
 }
 
 int mnb_device_status(unsigned *status_out, int clear) {

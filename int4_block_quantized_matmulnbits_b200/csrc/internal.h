@@ -73,6 +73,22 @@ int launch_gptq_prepare(const float *H, int64_t K, float percdamp, float *U, uin
 int launch_gptq_quantize(const float *W, const float *U, const uint8_t *dead, int64_t N, int64_t K, int bs,
                          int has_zp, uint8_t *packed, void *scales, int scale_f16, uint8_t *zp, cudaStream_t s);
 
+// A paged key-value cache: bookkeeping, norm + rotary + append, decode attention.
+int launch_paged_tables(const int32_t *ctx, const int32_t *neu, int B, int page, int num_pages,
+                        const int32_t *free_pages, int num_free, const int32_t *free_start, int32_t *table,
+                        int64_t table_stride, int max_blocks, int32_t *seq, int32_t *cu, int32_t *slots, int32_t *pos,
+                        int T, int32_t *free_next, int *status, unsigned flags, cudaStream_t s);
+int launch_rope_append(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs,
+                       const void *v, int64_t v_ts, int64_t v_hs, const mnb_paged_cache *c, const int32_t *slots,
+                       const int32_t *pos, int64_t T, int Hq, const float *cos, const float *sin, int R, int num_pos,
+                       const float *qw, const float *kw, float eps, void *q_out, int64_t o_ts, int64_t o_hs,
+                       int *status, unsigned flags, cudaStream_t s);
+size_t paged_attention_workspace_bytes(int Hq, int Hkv, int D, int f16);
+int launch_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_paged_cache *c, const int32_t *table,
+                           int64_t table_stride, int max_blocks, const int32_t *lens, int B, int Hq, float scale,
+                           void *out, int64_t o_bs, int64_t o_hs, float *lse, void *workspace, int *status,
+                           unsigned flags, cudaStream_t s);
+
 int read_device_status(unsigned *out, int clear);
 int read_gemv_status(unsigned *out, int clear);     // ORs the decode kernel's word into *out
 int read_res_status(unsigned *out, int clear);      // same for the one-token resident decode kernel

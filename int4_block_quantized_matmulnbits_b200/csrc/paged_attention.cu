@@ -1,0 +1,848 @@
+// paged_attention.cu -- attention of one new token per request over a paged
+// key-value cache (mnb_paged_attention).
+//
+// For request b, query head i of KV head h = i / G and the n = seq_lens[b] rows
+// of the cache that the block table names:
+//   s_j = scale * q_i . k_j,  lse = log sum_j exp(s_j),  o_i = sum_j exp(s_j - lse) v_j.
+// One pass over K and V with the running maximum m and sum l of the softmax:
+// on a new maximum, l and the accumulated o are scaled by exp(m_old - m_new).
+// Two such (m, l, o) over disjoint keys join the same way, so the cache's
+// length may be cut anywhere.
+//
+// Work split.  The keys of every (request, KV head, row tile of query heads) --
+// a segment -- are cut into tiles of TK keys.  All tiles of the call, in the
+// order (request, segment, tile), form one list that is cut into equal
+// contiguous ranges, one per CTA, and each CTA's range again into one per warp:
+// every warp streams the same number of tiles (+-1) whatever the lengths are.
+// A segment inside one warp's range is finished there; one that crosses warps
+// is joined in shared memory, one that crosses CTAs through the workspace, by
+// the CTA that arrives last, in CTA order (the result does not depend on which
+// CTA that is).
+//
+// Each warp owns a ring of STAGES tiles in shared memory that it fills with
+// 16-byte cp.async (rows behind the length and rows of page ids outside the
+// pool are zero-filled and masked, never read) and drains by itself: the main
+// loop has no CTA barrier, and the next segment's query rows (a stage of their
+// own) and first tiles are in flight while the current one ends.
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace mnb {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnParams {
+    const void *q, *k, *v;
+    void *out;
+    float *lse;
+    const int32_t *table, *lens;
+    int *counters;      // workspace: arrivals for the one segment that crosses the end of a CTA's range and
+                        // begins inside it, one count per CTA, zero between calls
+    float *partials;    // workspace: two partial results per CTA
+    int *status;
+    int64_t q_bs, q_hs, o_bs, o_hs;                        // elements
+    int64_t table_stride, page_stride, slot_stride, head_stride;
+    int B, G, Hkv, D, rows, row_tiles, page, num_pages, cap;   // cap: rows the table has room for
+    int min_tiles;                                         // fewest tiles worth a CTA
+    float scale;
+};
+
+// Element type, padded head size, rows of query heads per segment.
+template <typename T_, int DP_, int ROWS_, int STAGES_>
+struct Cfg {
+    using T = T_;
+    static constexpr bool F16 = std::is_same<T, half>::value;
+    static constexpr int DP = DP_, ROWS = ROWS_, STAGES = STAGES_;
+    static constexpr int TK = F16 ? 16 : 8;                 // keys per tile
+    static constexpr int NCH = DP * (int)sizeof(T) / 16;    // 16-byte chunks per row
+    static constexpr int ROW_BYTES = DP * (int)sizeof(T);
+    static constexpr int TILE_BYTES = TK * ROW_BYTES;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 r;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float dot(float4 a, float4 b, float c) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+__device__ __forceinline__ void fma4(float4 &c, float s, float4 v) {
+    c.x = fmaf(s, v.x, c.x), c.y = fmaf(s, v.y, c.y), c.z = fmaf(s, v.z, c.z), c.w = fmaf(s, v.w, c.w);
+}
+
+// A position in the list of tiles.
+struct Cursor {
+    int b, seg, tile, tiles;   // request, segment in it, tile in it, tiles per segment of b
+};
+
+struct Shared {
+    const uint32_t *prefix;    // [B + 1] tiles (of one segment) before request b
+    int B, NS;                 // NS = segments per request
+};
+
+__device__ __forceinline__ Cursor cursor_at(const Shared &sh, int64_t t) {
+    Cursor c;
+    int64_t u = t / sh.NS;   // among the requests' tiles of one segment each
+    int lo = 0, hi = sh.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)sh.prefix[mid + 1] > u)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    c.b = lo;
+    c.tiles = (int)(sh.prefix[lo + 1] - sh.prefix[lo]);
+    const int64_t r = t - (int64_t)sh.prefix[lo] * sh.NS;
+    c.seg = (int)(r / c.tiles);
+    c.tile = (int)(r - (int64_t)c.seg * c.tiles);
+    return c;
+}
+
+// The next tile; the caller knows that there is one.
+__device__ __forceinline__ void advance(const Shared &sh, Cursor &c) {
+    if (++c.tile < c.tiles)
+        return;
+    c.tile = 0;
+    if (++c.seg < sh.NS)
+        return;
+    c.seg = 0;
+    do {
+        c.b++;
+        c.tiles = (int)(sh.prefix[c.b + 1] - sh.prefix[c.b]);
+    } while (c.tiles == 0);
+}
+
+// The running softmax of one segment in a warp's registers.
+template <typename C, bool F16>
+struct Acc;
+
+// fp16: S = Q K^T and O += P V as m16n8k16 products with the query heads as the
+// 16 rows (rows at and above ROWS are zero).  P is rounded to fp16 with its
+// row's maximum at 2^10, so that terms down to 2^-24 of the largest keep their
+// 11 bits; l is summed from the unrounded fp32 values.
+template <typename C>
+struct Acc<C, true> {
+    static constexpr int HALVES = C::ROWS > 8 ? 2 : 1;
+    static constexpr float SHIFT = 10.0f;
+    float o[C::DP / 8][4];
+    float m[2], l[2];
+    uint32_t q[C::DP / 16][2 * HALVES];   // A fragments of the segment's query rows
+
+    // The segment's query rows, just landed at `qs`.
+    __device__ __forceinline__ void open(uint32_t qs, uint32_t, int rows) {
+        const int lane = threadIdx.x & 31;
+        const int qr = min((lane & 7) + (HALVES == 2 ? ((lane >> 3) & 1) * 8 : 0), rows - 1), qc = lane >> 4;
+#pragma unroll
+        for (int kk = 0; kk < C::DP / 16; kk++) {
+            uint32_t a0, a1, a2, a3;
+            ldsm4(qs + qr * C::ROW_BYTES + (((kk * 2 + qc) ^ (qr & 7)) << 4), a0, a1, a2, a3);
+            q[kk][0] = a0, q[kk][1] = a2;
+            if (HALVES == 2)
+                q[kk][HALVES] = a1, q[kk][HALVES + 1] = a3;
+        }
+        reset();
+    }
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int n = 0; n < C::DP / 8; n++)
+            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
+    }
+
+    // One tile: K and V in shared memory, `valid` one bit per key.
+    __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t, int, uint32_t valid, float scale2) {
+        const int lane = threadIdx.x & 31, t2 = (lane & 3) * 2;
+        float s[2][4] = {};
+        const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+#pragma unroll
+        for (int kk = 0; kk < C::DP / 16; kk++) {
+            uint32_t b0, b1, b2, b3;
+            const uint32_t a0 = q[kk][0], a2 = q[kk][1];
+            const uint32_t a1 = HALVES == 2 ? q[kk][HALVES] : 0u, a3 = HALVES == 2 ? q[kk][2 * HALVES - 1] : 0u;
+            ldsm4(ks + kr * C::ROW_BYTES + (((kk * 2 + kc) ^ (kr & 7)) << 4), b0, b1, b2, b3);
+            mma16816(s[0], a0, a1, a2, a3, b0, b1);
+            mma16816(s[1], a0, a1, a2, a3, b2, b3);
+        }
+        float mn[2] = {m[0], m[1]};
+#pragma unroll
+        for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                const bool ok = (valid >> (n * 8 + t2 + (c & 1))) & 1;
+                s[n][c] = ok ? s[n][c] * scale2 : -INFINITY;
+                mn[c >> 1] = fmaxf(mn[c >> 1], s[n][c]);
+            }
+        uint32_t p[2][2];   // [key half][row half], packed pairs
+        bool grew = false;
+#pragma unroll
+        for (int h = 0; h < HALVES; h++) {
+            mn[h] = fmaxf(mn[h], __shfl_xor_sync(0xffffffffu, mn[h], 1));
+            mn[h] = fmaxf(mn[h], __shfl_xor_sync(0xffffffffu, mn[h], 2));
+            grew |= mn[h] > m[h];
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int h = 0; h < HALVES; h++) {
+                const float alpha = mn[h] > m[h] ? ex2(m[h] - mn[h]) : 1.0f;   // 0 after m = -inf
+                m[h] = mn[h];
+                l[h] *= alpha;
+#pragma unroll
+                for (int n = 0; n < C::DP / 8; n++)
+                    o[n][2 * h] *= alpha, o[n][2 * h + 1] *= alpha;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < HALVES; h++) {
+            const float base = m[h] == -INFINITY ? 0.0f : m[h] - SHIFT;
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                const float x = ex2(s[n][2 * h] - base), y = ex2(s[n][2 * h + 1] - base);
+                l[h] += x + y;
+                p[n][h] = h2_as_u32(__floats2half2_rn(x, y));
+            }
+        }
+        if (HALVES == 1)
+            p[0][1] = p[1][1] = 0;
+        const int vr = lane & 15, vc = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < C::DP / 16; n++) {
+            uint32_t b0, b1, b2, b3;
+            ldsm4t(vs + vr * C::ROW_BYTES + (((n * 2 + vc) ^ (vr & 7)) << 4), b0, b1, b2, b3);
+            mma16816(o[2 * n], p[0][0], p[0][1], p[1][0], p[1][1], b0, b1);
+            mma16816(o[2 * n + 1], p[0][0], p[0][1], p[1][0], p[1][1], b2, b3);
+        }
+    }
+
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int h = 0; h < HALVES; h++) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+    }
+
+    // f(row, column, value, value) over pairs of columns; g(row, m, l) once per row.
+    template <typename F, typename H>
+    __device__ __forceinline__ void each(F f, H g) {
+        const int lane = threadIdx.x & 31, r0 = lane >> 2, t2 = (lane & 3) * 2;
+#pragma unroll
+        for (int h = 0; h < HALVES; h++) {
+#pragma unroll
+            for (int n = 0; n < C::DP / 8; n++)
+                f(r0 + 8 * h, n * 8 + t2, o[n][2 * h], o[n][2 * h + 1], m[h], l[h]);
+            if (t2 == 0)
+                g(r0 + 8 * h, m[h], l[h]);
+        }
+    }
+    static constexpr float kSumScale = 1.0f / 1024.0f;   // 2^-SHIFT
+};
+
+// fp32: every product and sum in fp32 on the CUDA cores.  Scores: a lane holds
+// key lane % 8 and a quarter of the chunks, two shuffles add the quarters.
+// Output: a lane holds whole columns; a row's probabilities come by shuffle.
+template <typename C>
+struct Acc<C, false> {
+    static constexpr int LPR = C::NCH < 32 ? C::NCH : 32;   // lanes per row of V
+    static constexpr int PER = C::NCH / LPR;                // chunks a lane holds
+    static constexpr int KSPLIT = 32 / LPR;                 // keys taken at a time
+    float4 o[C::ROWS][PER];
+    float m[C::ROWS], l[C::ROWS];
+
+    // The segment's query rows, just landed at `land`: kept at `qs`.
+    __device__ __forceinline__ void open(uint32_t land, uint32_t qs, int rows) {
+        __syncwarp();   // the last segment's rows have been read
+        for (int i = threadIdx.x & 31; i < rows * C::NCH; i += 32) {
+            const float4 v = lds4(land + i * 16);
+            asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(qs + i * 16), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                         : "memory");
+        }
+        __syncwarp();
+        reset();
+    }
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int r = 0; r < C::ROWS; r++) {
+#pragma unroll
+            for (int c = 0; c < PER; c++)
+                o[r][c] = make_float4(0, 0, 0, 0);
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+        }
+    }
+
+    __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t qs, int rows, uint32_t valid, float scale2) {
+        const int lane = threadIdx.x & 31, key = lane & 7, quarter = lane >> 3;
+        float s[C::ROWS] = {};
+#pragma unroll 4
+        for (int c = 0; c < C::NCH / 4; c++) {
+            const int ch = c * 4 + quarter;
+            const float4 k = lds4(ks + key * C::ROW_BYTES + ((ch ^ key) << 4));
+#pragma unroll
+            for (int r = 0; r < C::ROWS; r++) {
+                const int qr = min(r, rows - 1);
+                s[r] = dot(k, lds4(qs + qr * C::ROW_BYTES + ((ch ^ (qr & 7)) << 4)), s[r]);
+            }
+        }
+        const bool ok = (valid >> key) & 1;
+#pragma unroll
+        for (int r = 0; r < C::ROWS; r++) {
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 8);
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
+            s[r] = ok ? s[r] * scale2 : -INFINITY;
+            float mn = fmaxf(m[r], s[r]);
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1)
+                mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+            if (mn > m[r]) {   // the same in every lane
+                const float alpha = ex2(m[r] - mn);
+                m[r] = mn;
+                l[r] *= alpha;
+#pragma unroll
+                for (int c = 0; c < PER; c++)
+                    o[r][c].x *= alpha, o[r][c].y *= alpha, o[r][c].z *= alpha, o[r][c].w *= alpha;
+            }
+            s[r] = mn == -INFINITY ? 0.0f : ex2(s[r] - mn);
+            l[r] += s[r];   // this lane's key; the eight keys are added in finish()
+        }
+        const int col = lane % LPR, sub = lane / LPR;
+#pragma unroll
+        for (int j = 0; j < 8; j += KSPLIT) {
+            const int kj = j + sub;
+            float4 v[PER];
+#pragma unroll
+            for (int c = 0; c < PER; c++)
+                v[c] = lds4(vs + kj * C::ROW_BYTES + (((col + c * 32) ^ kj) << 4));
+#pragma unroll
+            for (int r = 0; r < C::ROWS; r++) {
+                const float pr = __shfl_sync(0xffffffffu, s[r], kj);
+#pragma unroll
+                for (int c = 0; c < PER; c++)
+                    fma4(o[r][c], pr, v[c]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int r = 0; r < C::ROWS; r++) {
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1)
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+#pragma unroll
+            for (int c = 0; c < PER; c++)
+#pragma unroll
+                for (int x = LPR; x < 32; x <<= 1) {
+                    o[r][c].x += __shfl_xor_sync(0xffffffffu, o[r][c].x, x);
+                    o[r][c].y += __shfl_xor_sync(0xffffffffu, o[r][c].y, x);
+                    o[r][c].z += __shfl_xor_sync(0xffffffffu, o[r][c].z, x);
+                    o[r][c].w += __shfl_xor_sync(0xffffffffu, o[r][c].w, x);
+                }
+        }
+    }
+
+    template <typename F, typename H>
+    __device__ __forceinline__ void each(F f, H g) {
+        const int lane = threadIdx.x & 31, col = lane % LPR;
+        if (lane >= LPR)
+            return;
+#pragma unroll
+        for (int r = 0; r < C::ROWS; r++) {
+#pragma unroll
+            for (int c = 0; c < PER; c++) {
+                const int e = (col + c * 32) * 4;
+                f(r, e, o[r][c].x, o[r][c].y, m[r], l[r]);
+                f(r, e + 2, o[r][c].z, o[r][c].w, m[r], l[r]);
+            }
+            if (lane == 0)
+                g(r, m[r], l[r]);
+        }
+    }
+    static constexpr float kSumScale = 1.0f;
+};
+
+// Two neighbouring outputs of one row; c is even and below D (a multiple of 8).
+__device__ __forceinline__ void store2(half *p, float a, float b) { *reinterpret_cast<half2 *>(p) = __floats2half2_rn(a, b); }
+__device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
+
+// log sum exp from a maximum in log2 units and a sum relative to it.
+__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? m * kLn2 + logf(l) : -INFINITY; }
+
+// A partial result in memory: rows x D outputs, then rows maxima, then rows sums
+// (relative to the maximum, as o is).
+__host__ __device__ __forceinline__ int64_t partial_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
+
+// First tile of the i-th of n equal ranges of `total` tiles.
+__device__ __forceinline__ int64_t range_at(int64_t total, int n, int i) {
+    return total / n * i + min((int64_t)i, total % n);
+}
+// The range that holds tile t (0 <= t < total).
+__device__ __forceinline__ int range_of(int64_t total, int n, int64_t t) {
+    const int64_t q = total / n, r = total % n, cut = r * (q + 1);
+    return (int)(t < cut ? t / (q + 1) : r + (t - cut) / q);
+}
+
+template <typename C>
+__global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_constant__ AttnParams p) {
+    using T = typename C::T;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kRing = C::STAGES * 2 * C::TILE_BYTES;   // bytes a warp
+    uint8_t *ring = smem + (size_t)warp * kRing;
+    const int q_bytes = C::F16 ? 0 : p.rows * C::ROW_BYTES;   // fp32 only: the current query rows
+    const uint32_t q_keep = smem_u32(smem) + kWarps * kRing + warp * q_bytes;
+    const int pf = (int)partial_floats(p.rows, p.D);
+    // a warp's partial results: [0] of the segment that its range begins inside
+    // of, [1] of the one that it opens and does not end, in its drained ring
+    float *heads = reinterpret_cast<float *>(smem + kWarps * (kRing + q_bytes));   // [kWarps][pf]
+    auto slot_of = [&](int w, int opened) {
+        return opened ? reinterpret_cast<float *>(smem + (size_t)w * kRing) : heads + w * pf;
+    };
+    uint32_t *prefix = reinterpret_cast<uint32_t *>(heads + kWarps * pf);                       // [B + 1]
+    __shared__ uint32_t warp_sums[kWarps];
+    __shared__ int last_seg[2];
+
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // tiles of each request, and their sums
+    uint32_t carry = 0;
+    bool bad_len = false;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + (int)threadIdx.x;
+        uint32_t v = 0;
+        if (b < p.B) {
+            const int n = p.lens[b];
+            bad_len |= n < 0 || n > p.cap;
+            v = (uint32_t)(min(max(n, 0), p.cap) + C::TK - 1) / C::TK;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o)
+                v += u;
+        }
+        __syncthreads();
+        if (lane == 31)
+            warp_sums[warp] = v;
+        __syncthreads();
+        uint32_t before = carry;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            before += w < warp ? warp_sums[w] : 0u;
+            carry += warp_sums[w];
+        }
+        if (b < p.B)
+            prefix[b + 1] = v + before;
+    }
+    if (threadIdx.x == 0) {
+        prefix[0] = 0;
+        last_seg[0] = last_seg[1] = -1;
+    }
+    if (bad_len && blockIdx.x == 0 && p.status)
+        atomicOr(p.status, 2);
+    __syncthreads();
+
+    Shared sh;
+    sh.prefix = prefix, sh.B = p.B, sh.NS = p.Hkv * p.row_tiles;
+    const int Hq = p.Hkv * p.G;
+
+    // requests without a key: zero rows
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+        if (prefix[b + 1] == prefix[b]) {
+            for (int i = threadIdx.x; i < Hq * (p.D / 2); i += kThreads)
+                store2((T *)p.out + b * p.o_bs + (i / (p.D / 2)) * p.o_hs + (i % (p.D / 2)) * 2, 0.0f, 0.0f);
+            if (p.lse)
+                for (int i = threadIdx.x; i < Hq; i += kThreads)
+                    p.lse[(int64_t)b * Hq + i] = -INFINITY;
+        }
+
+    const int64_t total = (int64_t)prefix[p.B] * sh.NS;
+    int64_t want = (total + p.min_tiles - 1) / p.min_tiles;
+    const int nc = (int)min((int64_t)gridDim.x, max(want, (int64_t)1));
+    if ((int)blockIdx.x >= nc || total == 0)
+        return;
+    const int64_t c0 = range_at(total, nc, blockIdx.x), c1 = range_at(total, nc, blockIdx.x + 1);
+    const int64_t w0 = c0 + range_at(c1 - c0, kWarps, warp), w1 = c0 + range_at(c1 - c0, kWarps, warp + 1);
+    const float scale2 = p.scale * kLog2e;
+
+    // where the row of query head `r` of segment `seg` goes
+    auto out_row = [&](int b, int seg, int r) -> int {   // query head, or -1 past the group
+        const int h = seg / p.row_tiles, i = (seg - h * p.row_tiles) * C::ROWS + r;
+        return r < p.rows && i < p.G ? h * p.G + i : -1;
+    };
+
+    if (w0 < w1) {
+        int left = (int)(w1 - w0), todo = left;   // tiles to issue, tiles to compute
+        Cursor load = cursor_at(sh, w0), cur = load;
+        bool load_q = true, cur_q = true;         // the segment's query rows come first
+        int len = min(p.lens[load.b], p.cap);
+        // the next tile's table entries, on the way while earlier tiles are issued: lane i holds key i
+        int ent = -1, ent_off = 0;
+        auto fetch = [&]() {
+            const int key = load.tile * C::TK + lane;
+            ent = -1;
+            if (lane < C::TK && key < len) {
+                const int blk = key / p.page;
+                ent_off = key - blk * p.page;
+                ent = p.table[load.b * p.table_stride + blk];
+            }
+        };
+        // Starts the copies of the next item (query rows or a tile) into a stage; the tile's valid keys.
+        auto issue = [&](int stage) -> uint32_t {
+            const int h = load.seg / p.row_tiles;
+            const uint32_t ks = smem_u32(ring) + stage * 2 * C::TILE_BYTES, vs = ks + C::TILE_BYTES;
+            constexpr int EPC = 16 / (int)sizeof(T);                 // elements per chunk
+            if (load_q) {
+                load_q = false;
+                for (int i = lane; i < p.rows * C::NCH; i += 32) {
+                    const int r = i / C::NCH, ch = i % C::NCH, e = ch * EPC;
+                    const int head = out_row(load.b, load.seg, r);
+                    const bool in = head >= 0 && e < p.D;
+                    const T *src = (const T *)p.q + (in ? load.b * p.q_bs + head * p.q_hs + e : 0);
+                    cp_async16(ks + r * C::ROW_BYTES + ((ch ^ (r & 7)) << 4), src, in ? 16 : 0);
+                }
+                return 0;
+            }
+            bool has = ent >= 0 && ent < p.num_pages;
+            if (!has && lane < C::TK && load.tile * C::TK + lane < len && p.status)
+                atomicOr(p.status, 1);
+            const uint32_t valid = __ballot_sync(0xffffffffu, has);
+            const int64_t off = has ? ent * p.page_stride + ent_off * p.slot_stride + h * p.head_stride : 0;
+            constexpr int RPI = C::NCH >= 32 ? 1 : 32 / C::NCH;      // rows per instruction
+            constexpr int CPL = C::NCH > 32 ? C::NCH / 32 : 1;       // chunks of a row per lane
+            const int sub = C::NCH >= 32 ? 0 : lane / C::NCH, ch0 = C::NCH >= 32 ? lane : lane % C::NCH;
+#pragma unroll
+            for (int j = 0; j < C::TK / RPI; j++) {
+                const int row = j * RPI + sub;
+                const int64_t ro = __shfl_sync(0xffffffffu, off, row);
+                const bool ok = (valid >> row) & 1;
+#pragma unroll
+                for (int c = 0; c < CPL; c++) {
+                    const int ch = ch0 + c * 32, e = ch * EPC;
+                    const bool in = ok && e < p.D;
+                    const int64_t at = in ? ro + e : 0;
+                    const uint32_t d = row * C::ROW_BYTES + ((ch ^ (row & 7)) << 4);
+                    cp_async16(ks + d, (const T *)p.k + at, in ? 16 : 0);
+                    cp_async16(vs + d, (const T *)p.v + at, in ? 16 : 0);
+                }
+            }
+            if (--left > 0) {
+                const int b = load.b;
+                advance(sh, load);
+                load_q = load.tile == 0;
+                if (load.b != b)
+                    len = min(p.lens[load.b], p.cap);
+                fetch();
+            }
+            return valid;
+        };
+        Acc<C, C::F16> acc;
+        uint32_t vmask[C::STAGES - 1];   // valid keys of the items in flight
+        fetch();
+#pragma unroll
+        for (int s = 0; s < C::STAGES - 1; s++) {
+            vmask[s] = left > 0 ? issue(s) : 0u;
+            cp_commit();
+        }
+        bool opened = cur.tile == 0;   // the segment's first tile is this warp's
+        int stage = 0;
+        while (todo > 0) {
+            cp_wait<C::STAGES - 2>();
+            __syncwarp();
+            const int ahead = stage == 0 ? C::STAGES - 1 : stage - 1;   // the stage that the last item left
+            const uint32_t nv = left > 0 ? issue(ahead) : 0u;
+            cp_commit();
+            const uint32_t ks = smem_u32(ring) + stage * 2 * C::TILE_BYTES;
+            const uint32_t valid = vmask[0];
+#pragma unroll
+            for (int s = 0; s + 1 < C::STAGES - 1; s++)
+                vmask[s] = vmask[s + 1];
+            vmask[C::STAGES - 2] = nv;
+            stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+            if (cur_q) {
+                cur_q = false;
+                acc.open(ks, q_keep, p.rows);
+                continue;
+            }
+            acc.tile(ks, ks + C::TILE_BYTES, q_keep, p.rows, valid, scale2);
+            todo--;
+            const bool ends = cur.tile + 1 == cur.tiles;
+            if (ends || todo == 0) {
+                acc.finish();
+                if (opened && ends) {
+                    T *o = (T *)p.out + cur.b * p.o_bs;
+                    acc.each(
+                        [&](int r, int c, float x, float y, float, float l) {
+                            const int head = out_row(cur.b, cur.seg, r);
+                            if (head >= 0 && c < p.D) {
+                                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                                store2(o + head * p.o_hs + c, x * inv, y * inv);
+                            }
+                        },
+                        [&](int r, float m, float l) {
+                            const int head = out_row(cur.b, cur.seg, r);
+                            if (head >= 0 && p.lse)
+                                p.lse[(int64_t)cur.b * Hq + head] = lse_of(m, l * Acc<C, C::F16>::kSumScale);
+                        });
+                } else {
+                    __syncwarp();   // every lane has read the last tile of a ring that is written over
+                    float *sl = slot_of(warp, opened);
+                    acc.each(
+                        [&](int r, int c, float x, float y, float, float) {
+                            if (r < p.rows && c < p.D)
+                                *reinterpret_cast<float2 *>(sl + r * p.D + c) = make_float2(x, y);
+                        },
+                        [&](int r, float m, float l) {
+                            if (r < p.rows) {
+                                sl[p.rows * p.D + r] = m;
+                                sl[p.rows * p.D + p.rows + r] = l;
+                            }
+                        });
+                }
+                opened = true;
+                cur_q = true;
+            }
+            if (todo > 0)
+                advance(sh, cur);
+        }
+    }
+    __syncthreads();
+
+    // Joins n partials: part(i) is the i-th.  All threads of a warp (or of the
+    // CTA, with `tid` and `nt`) take part; sink(r, c, o, l, m) gets each output
+    // before its division by l.
+    auto join = [&](int np, auto part, int tid, int nt, auto sink) {
+        for (int e = tid * 2; e < p.rows * p.D; e += nt * 2) {
+            const int r = e / p.D;
+            float M = -INFINITY;
+            for (int i = 0; i < np; i++)
+                M = fmaxf(M, __ldcg(part(i) + p.rows * p.D + r));
+            const float base = M == -INFINITY ? 0.0f : M;
+            float x = 0.0f, y = 0.0f, l = 0.0f;
+            for (int i = 0; i < np; i++) {
+                const float *q = part(i);
+                const float w = ex2(__ldcg(q + p.rows * p.D + r) - base);
+                const float2 o = __ldcg(reinterpret_cast<const float2 *>(q + e));
+                x = fmaf(w, o.x, x), y = fmaf(w, o.y, y);
+                l = fmaf(w, __ldcg(q + p.rows * p.D + p.rows + r), l);
+            }
+            sink(r, e - r * p.D, x, y, M, l);
+        }
+    };
+    auto write_out = [&](int b, int seg, int r, int c, float x, float y, float M, float l) {
+        const int head = out_row(b, seg, r);
+        if (head < 0)
+            return;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        store2((T *)p.out + b * p.o_bs + head * p.o_hs + c, x * inv, y * inv);
+        if (c == 0 && p.lse)
+            p.lse[(int64_t)b * Hq + head] = lse_of(M, l * Acc<C, C::F16>::kSumScale);
+    };
+
+    // segments that cross warps: the one that the CTA's range begins inside of
+    // (warp 0), and the one whose first tile is in this warp but not its last
+    for (int kind = 0; kind < 2; kind++) {
+        if (w0 >= w1 || (kind == 0 && warp != 0))
+            continue;
+        const Cursor cu = cursor_at(sh, kind == 0 ? c0 : w1 - 1);
+        const int64_t at = kind == 0 ? c0 : w1 - 1;
+        const int64_t first = at - cu.tile, end = first + cu.tiles;   // the segment's tiles
+        if (kind == 0 ? cu.tile == 0 : (first < w0 || end <= w1))
+            continue;
+        const int64_t stop = min(end, c1);
+        const int wl = range_of(c1 - c0, kWarps, stop - 1 - c0);
+        const bool whole = first >= c0 && end <= c1;
+        float *dst = p.partials + ((int64_t)blockIdx.x * 2 + kind) * pf;
+        auto part = [&](int i) -> const float * { return slot_of(warp + i, kind == 1 && i == 0); };
+        const int np = wl - warp + 1;
+        for (int e = lane * 2; e < p.rows * p.D; e += 64) {
+            const int r = e / p.D;
+            float M = -INFINITY;
+            for (int i = 0; i < np; i++)
+                M = fmaxf(M, part(i)[p.rows * p.D + r]);
+            const float base = M == -INFINITY ? 0.0f : M;
+            float x = 0.0f, y = 0.0f, l = 0.0f;
+            for (int i = 0; i < np; i++) {
+                const float *q = part(i);
+                const float w = ex2(q[p.rows * p.D + r] - base);
+                const float2 o = *reinterpret_cast<const float2 *>(q + e);
+                x = fmaf(w, o.x, x), y = fmaf(w, o.y, y), l = fmaf(w, q[p.rows * p.D + p.rows + r], l);
+            }
+            if (whole) {
+                write_out(cu.b, cu.seg, r, e - r * p.D, x, y, M, l);
+            } else {
+                *reinterpret_cast<float2 *>(dst + e) = make_float2(x, y);
+                if (e == r * p.D) {
+                    dst[p.rows * p.D + r] = M;
+                    dst[p.rows * p.D + p.rows + r] = l;
+                }
+            }
+        }
+        if (!whole) {
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) {
+                const int cf = range_of(total, nc, first), cl = range_of(total, nc, end - 1);
+                const int id = cu.b * sh.NS + cu.seg;
+                if (atomicAdd(p.counters + cf, 1) == cl - cf) {
+                    p.counters[cf] = 0;
+                    last_seg[kind] = id;
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    // segments that cross CTAs and whose last part was written here
+    for (int kind = 0; kind < 2; kind++) {
+        const int id = last_seg[kind];
+        if (id < 0)
+            continue;
+        __threadfence();
+        const int b = id / sh.NS, seg = id - b * sh.NS;
+        const int tiles = (int)(prefix[b + 1] - prefix[b]);
+        const int64_t first = (int64_t)prefix[b] * sh.NS + (int64_t)seg * tiles;
+        const int cf = range_of(total, nc, first), cl = range_of(total, nc, first + tiles - 1);
+        auto part = [&](int i) -> const float * { return p.partials + ((int64_t)(cf + i) * 2 + (i == 0 ? 1 : 0)) * pf; };
+        join(cl - cf + 1, part, threadIdx.x, kThreads, [&](int r, int c, float x, float y, float M, float l) {
+            write_out(b, seg, r, c, x, y, M, l);
+        });
+    }
+}
+
+constexpr size_t kSmemMax = 227 * 1024 - 256;
+constexpr size_t kSmemTwo = 113 * 1024 - 256;   // two CTAs on an SM
+
+template <typename C>
+int launch_cfg(const AttnParams &p, int most, size_t smem, unsigned flags, cudaStream_t s) {
+    const int resident = device_sm_count() * (smem <= kSmemTwo ? 2 : 1);
+    const int grid = most < resident ? most : resident;
+    static int cache[kMaxDevices] = {};
+    auto *kernel = paged_attention_kernel<C>;
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)smem, cache);
+    if (e != cudaSuccess)
+        return fail(MNB_ERR_CUDA, "mnb_paged_attention: %s", cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    if (flags & MNB_FLAG_PDL) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
+        cfg.attrs = attr;
+    }
+    e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess)
+        return fail(MNB_ERR_CUDA, "mnb_paged_attention: launch: %s", cudaGetErrorString(e));
+    return MNB_OK;
+}
+
+// Shared memory of a CTA.
+template <typename C>
+size_t smem_bytes(int rows, int D, int B) {
+    return (size_t)kWarps * (C::STAGES * 2 * C::TILE_BYTES + (C::F16 ? 0 : rows * C::ROW_BYTES)) +
+           (size_t)kWarps * partial_floats(rows, D) * 4 + (size_t)(B + 1) * 4;
+}
+
+template <typename T, int DP, int ROWS>
+int launch_rows(const AttnParams &p, int most, unsigned flags, cudaStream_t s) {
+    using C2 = Cfg<T, DP, ROWS, 2>;
+    using C3 = Cfg<T, DP, ROWS, 3>;
+    const size_t s2 = smem_bytes<C2>(p.rows, p.D, p.B), s3 = smem_bytes<C3>(p.rows, p.D, p.B);
+    if (s3 <= kSmemTwo)
+        return launch_cfg<C3>(p, most, s3, flags, s);
+    if (s2 > kSmemMax)
+        return fail(MNB_ERR_UNSUPPORTED, "mnb_paged_attention: %zu bytes of shared memory needed", s2);
+    return launch_cfg<C2>(p, most, s2, flags, s);
+}
+
+template <typename T, int DP>
+int launch_dp(const AttnParams &p, int ctas, unsigned flags, cudaStream_t s) {
+    if constexpr (std::is_same<T, half>::value)
+        return p.rows > 8 ? launch_rows<T, DP, 16>(p, ctas, flags, s) : launch_rows<T, DP, 8>(p, ctas, flags, s);
+    else
+        return p.rows > 4   ? launch_rows<T, DP, 8>(p, ctas, flags, s)
+               : p.rows > 2 ? launch_rows<T, DP, 4>(p, ctas, flags, s)
+               : p.rows > 1 ? launch_rows<T, DP, 2>(p, ctas, flags, s)
+                            : launch_rows<T, DP, 1>(p, ctas, flags, s);
+}
+
+int rows_per_segment(int G, int f16) { return G < (f16 ? 16 : 8) ? G : (f16 ? 16 : 8); }
+int grid_of() { return device_sm_count() * 2; }
+size_t counters_bytes() { return ((size_t)grid_of() * 4 + 127) / 128 * 128; }
+
+}  // namespace
+
+size_t paged_attention_workspace_bytes(int Hq, int Hkv, int D, int f16) {
+    return counters_bytes() + (size_t)grid_of() * 2 * partial_floats(rows_per_segment(Hq / Hkv, f16), D) * 4;
+}
+
+int launch_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_paged_cache *c, const int32_t *table,
+                           int64_t table_stride, int max_blocks, const int32_t *lens, int B, int Hq, float scale,
+                           void *out, int64_t o_bs, int64_t o_hs, float *lse, void *workspace, int *status,
+                           unsigned flags, cudaStream_t s) {
+    const int f16 = c->dtype == MNB_F16;
+    AttnParams p;
+    p.q = q, p.k = c->k, p.v = c->v, p.out = out, p.lse = lse, p.table = table, p.lens = lens, p.status = status;
+    p.q_bs = q_bs, p.q_hs = q_hs, p.o_bs = o_bs, p.o_hs = o_hs, p.table_stride = table_stride;
+    p.page_stride = c->page_stride, p.slot_stride = c->slot_stride, p.head_stride = c->head_stride;
+    p.B = B, p.Hkv = (int)c->num_heads, p.G = Hq / p.Hkv, p.D = (int)c->head_dim;
+    p.rows = rows_per_segment(p.G, f16);
+    p.row_tiles = (p.G + p.rows - 1) / p.rows;
+    p.page = (int)c->page_size, p.num_pages = (int)c->num_pages, p.cap = max_blocks * p.page, p.scale = scale;
+    p.min_tiles = kWarps;
+    p.counters = (int *)workspace;
+    p.partials = (float *)((uint8_t *)workspace + counters_bytes());
+    // no more CTAs than the table's width could need
+    const int tk = f16 ? 16 : 8;
+    const int64_t most = ((int64_t)B * ((p.cap + tk - 1) / tk) * p.Hkv * p.row_tiles + p.min_tiles - 1) / p.min_tiles;
+    const int ctas = (int)(most < grid_of() ? (most < 1 ? 1 : most) : grid_of());
+    if (f16)
+        return p.D <= 64    ? launch_dp<half, 64>(p, ctas, flags, s)
+               : p.D <= 128 ? launch_dp<half, 128>(p, ctas, flags, s)
+                            : launch_dp<half, 256>(p, ctas, flags, s);
+    return p.D <= 64    ? launch_dp<float, 64>(p, ctas, flags, s)
+           : p.D <= 128 ? launch_dp<float, 128>(p, ctas, flags, s)
+                        : launch_dp<float, 256>(p, ctas, flags, s);
+}
+
+}  // namespace mnb
