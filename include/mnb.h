@@ -378,7 +378,7 @@ MNB_API int mnb_gptq_quantize(const float *W, const float *U, const uint8_t *dea
  *   bit 2  (mnb_paged_tables) the free list has run out. */
 typedef struct mnb_paged_cache {
     void *k, *v;            /* keys and values: row of (page, offset, head) at the strides below */
-    int64_t num_pages;      /* pages in the pool; num_pages * page_size < 2^31 */
+    int64_t num_pages;      /* pages in the pool; num_pages * page_size <= 2^31 - 64 */
     int64_t page_size;      /* tokens per page, any positive number */
     int64_t num_heads;      /* KV heads */
     int64_t head_dim;       /* entries of a head, contiguous; a multiple of 8, <= 256 */
@@ -450,7 +450,9 @@ MNB_API int mnb_rope_append(const void *q, int64_t q_token_stride, int64_t q_hea
  * that, n below 0 as 0 (status bit 1); keys of a page id outside the pool are
  * left out (bit 0).  Nothing behind a request's n tokens is read: entries of
  * the block table and rows of its last page there may hold anything.
- *   lse fp32 [B][Hq] or NULL.  1 <= Hq <= 4096, Hq % Hkv == 0, 0 <= B <= 4096.
+ *   lse fp32 [B][Hq] or NULL.  1 <= Hq <= 4096, Hq % Hkv == 0, 0 <= B <= 4096,
+ *   max_blocks * page_size <= 2^31 - 64, and B * Hq * max_blocks * page_size
+ *   below 2^34 (MNB_ERR_SHAPE may come later, where heads share).
  *   Results are the same, bit for bit, from call to call on one GPU model.
  * workspace: mnb_paged_attention_workspace_bytes (for the current device),
  * 16-byte aligned, ZERO-FILLED before its first use; its first bytes count

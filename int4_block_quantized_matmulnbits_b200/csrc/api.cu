@@ -119,9 +119,10 @@ static int check_matmul_args(const char *fn, const void *X, int act_t, const uin
     return MNB_OK;
 }
 
-// Limits of the paged cache: slots are int32, the request scans are one CTA's,
-// and page * stride stays far below 2^63.
-static const int64_t kMaxSlots = ((int64_t)1 << 31) - 1, kMaxRequests = 4096, kMaxHeads = 4096;
+// Limits of the paged cache: slots and positions are int32 and so is the end of
+// the tile that holds the last one, the request scans are one CTA's, and
+// page * stride stays far below 2^63.
+static const int64_t kMaxSlots = ((int64_t)1 << 31) - 64, kMaxRequests = 4096, kMaxHeads = 4096;
 static const int64_t kMaxStride = (int64_t)1 << 31;
 
 static int check_stride(const char *fn, int64_t stride, int dtype) {
@@ -140,7 +141,7 @@ static int check_paged_cache(const char *fn, const mnb_paged_cache *c) {
     if ((rc = check_dtype(fn, "cache", c->dtype)))
         return rc;
     if (c->page_size < 1 || c->num_pages < 1 || c->page_size > kMaxSlots || c->num_pages > kMaxSlots / c->page_size)
-        return fail(MNB_ERR_SHAPE, "%s: %lld pages of %lld tokens (at least one, below 2^31 tokens)", fn,
+        return fail(MNB_ERR_SHAPE, "%s: %lld pages of %lld tokens (at least one, at most 2^31 - 64 tokens)", fn,
                     (long long)c->num_pages, (long long)c->page_size);
     if (c->num_heads < 1 || c->num_heads > kMaxHeads)
         return fail(MNB_ERR_SHAPE, "%s: %lld KV heads", fn, (long long)c->num_heads);
@@ -511,7 +512,7 @@ int mnb_paged_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B
     if (B > kMaxRequests)
         return fail(MNB_ERR_UNSUPPORTED, "%s: B=%lld above %lld", fn, (long long)B, (long long)kMaxRequests);
     if (page_size < 1 || num_pages < 1 || page_size > kMaxSlots || num_pages > kMaxSlots / page_size)
-        return fail(MNB_ERR_SHAPE, "%s: %lld pages of %lld tokens (at least one, below 2^31 tokens)", fn,
+        return fail(MNB_ERR_SHAPE, "%s: %lld pages of %lld tokens (at least one, at most 2^31 - 64 tokens)", fn,
                     (long long)num_pages, (long long)page_size);
     if (max_blocks < 1 || max_blocks > kMaxSlots / page_size || table_stride < max_blocks || table_stride > kMaxStride)
         return fail(MNB_ERR_SHAPE, "%s: block table of %lld columns, row stride %lld", fn, (long long)max_blocks,
@@ -612,8 +613,6 @@ int mnb_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_pag
         table_stride > kMaxStride)
         return fail(MNB_ERR_SHAPE, "%s: block table of %lld columns, row stride %lld", fn, (long long)max_blocks,
                     (long long)table_stride);
-    if (B * ((max_blocks * cache->page_size + 7) / 8) > kMaxSlots)
-        return fail(MNB_ERR_SHAPE, "%s: B * max_blocks * page_size is 2^34 or more", fn);
     if (!(scale >= -3.0e38f && scale <= 3.0e38f))
         return fail(MNB_ERR_INVALID_ARG, "%s: scale is not finite", fn);
     if (flags & ~(unsigned)MNB_FLAG_PDL)

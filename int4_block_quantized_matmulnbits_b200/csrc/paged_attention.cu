@@ -49,7 +49,9 @@ struct AttnParams {
     int64_t q_bs, q_hs, o_bs, o_hs;                        // elements
     int64_t table_stride, page_stride, slot_stride, head_stride;
     int B, G, Hkv, D, rows, row_tiles, page, num_pages, cap;   // cap: rows the table has room for
+    int page_shift;                                        // log2(page), -1 if it is no power of two
     int min_tiles;                                         // fewest tiles worth a CTA
+    float join_cost;                                       // of a partial result in the last join, in tiles
     float scale;
 };
 
@@ -102,9 +104,10 @@ __device__ __forceinline__ void fma4(float4 &c, float s, float4 v) {
     c.x = fmaf(s, v.x, c.x), c.y = fmaf(s, v.y, c.y), c.z = fmaf(s, v.z, c.z), c.w = fmaf(s, v.w, c.w);
 }
 
-// A position in the list of tiles.
+// A position in the list of tiles (32 bits: the host refuses longer lists).
 struct Cursor {
-    int b, seg, tile, tiles;   // request, segment in it, tile in it, tiles per segment of b
+    int b, seg;              // request, segment in it
+    uint32_t tile, tiles;    // tile in the segment, tiles per segment of b
 };
 
 struct Shared {
@@ -112,22 +115,22 @@ struct Shared {
     int B, NS;                 // NS = segments per request
 };
 
-__device__ __forceinline__ Cursor cursor_at(const Shared &sh, int64_t t) {
+__device__ __forceinline__ Cursor cursor_at(const Shared &sh, uint32_t t) {
     Cursor c;
-    int64_t u = t / sh.NS;   // among the requests' tiles of one segment each
+    const uint32_t u = t / (uint32_t)sh.NS;   // among the requests' tiles of one segment each
     int lo = 0, hi = sh.B - 1;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if ((int64_t)sh.prefix[mid + 1] > u)
+        if (sh.prefix[mid + 1] > u)
             hi = mid;
         else
             lo = mid + 1;
     }
     c.b = lo;
-    c.tiles = (int)(sh.prefix[lo + 1] - sh.prefix[lo]);
-    const int64_t r = t - (int64_t)sh.prefix[lo] * sh.NS;
+    c.tiles = sh.prefix[lo + 1] - sh.prefix[lo];
+    const uint32_t r = t - sh.prefix[lo] * (uint32_t)sh.NS;
     c.seg = (int)(r / c.tiles);
-    c.tile = (int)(r - (int64_t)c.seg * c.tiles);
+    c.tile = r - (uint32_t)c.seg * c.tiles;
     return c;
 }
 
@@ -141,7 +144,7 @@ __device__ __forceinline__ void advance(const Shared &sh, Cursor &c) {
     c.seg = 0;
     do {
         c.b++;
-        c.tiles = (int)(sh.prefix[c.b + 1] - sh.prefix[c.b]);
+        c.tiles = sh.prefix[c.b + 1] - sh.prefix[c.b];
     } while (c.tiles == 0);
 }
 
@@ -404,38 +407,48 @@ __device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpre
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? m * kLn2 + logf(l) : -INFINITY; }
 
 // A partial result in memory: rows x D outputs, then rows maxima, then rows sums
-// (relative to the maximum, as o is).
-__host__ __device__ __forceinline__ int64_t partial_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
+// (relative to the maximum, as o is), to a multiple of 16 bytes.
+__host__ __device__ __forceinline__ int partial_floats(int rows, int D) { return (rows * (D + 2) + 3) / 4 * 4; }
 
 // First tile of the i-th of n equal ranges of `total` tiles.
-__device__ __forceinline__ int64_t range_at(int64_t total, int n, int i) {
-    return total / n * i + min((int64_t)i, total % n);
+__device__ __forceinline__ uint32_t range_at(uint32_t total, uint32_t n, uint32_t i) {
+    const uint32_t q = total / n;
+    return q * i + min(i, total - q * n);
 }
 // The range that holds tile t (0 <= t < total).
-__device__ __forceinline__ int range_of(int64_t total, int n, int64_t t) {
-    const int64_t q = total / n, r = total % n, cut = r * (q + 1);
-    return (int)(t < cut ? t / (q + 1) : r + (t - cut) / q);
+__device__ __forceinline__ uint32_t range_of(uint32_t total, uint32_t n, uint32_t t) {
+    const uint32_t q = total / n, r = total - q * n, cut = r * (q + 1);
+    return t < cut ? t / (q + 1) : r + (t - cut) / q;
 }
+
+// A segment that more than one warp or CTA works on, as one CTA sees it.
+struct Chain {
+    int warp, parts;         // its first warp here and the number of warps; parts = 0: none
+    int b, seg;
+    uint32_t first, end;     // its tiles in the list
+};
 
 template <typename C>
 __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_constant__ AttnParams p) {
     using T = typename C::T;
+    using A = Acc<C, C::F16>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kRing = C::STAGES * 2 * C::TILE_BYTES;   // bytes a warp
     uint8_t *ring = smem + (size_t)warp * kRing;
     const int q_bytes = C::F16 ? 0 : p.rows * C::ROW_BYTES;   // fp32 only: the current query rows
     const uint32_t q_keep = smem_u32(smem) + kWarps * kRing + warp * q_bytes;
-    const int pf = (int)partial_floats(p.rows, p.D);
+    const int pf = partial_floats(p.rows, p.D);
     // a warp's partial results: [0] of the segment that its range begins inside
     // of, [1] of the one that it opens and does not end, in its drained ring
     float *heads = reinterpret_cast<float *>(smem + kWarps * (kRing + q_bytes));   // [kWarps][pf]
-    auto slot_of = [&](int w, int opened) {
+    auto slot_of = [&](int w, bool opened) {
         return opened ? reinterpret_cast<float *>(smem + (size_t)w * kRing) : heads + w * pf;
     };
-    uint32_t *prefix = reinterpret_cast<uint32_t *>(heads + kWarps * pf);                       // [B + 1]
+    uint32_t *prefix = reinterpret_cast<uint32_t *>(heads + kWarps * pf);          // [B + 1]
     __shared__ uint32_t warp_sums[kWarps];
-    __shared__ int last_seg[2];
+    __shared__ Chain chains[kWarps + 1];   // [0] the segment that the CTA's range begins inside of, [1 + w] opened by warp w
+    __shared__ int last[2];
 
     pdl_wait();
     pdl_launch_dependents();
@@ -449,7 +462,7 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
         if (b < p.B) {
             const int n = p.lens[b];
             bad_len |= n < 0 || n > p.cap;
-            v = (uint32_t)(min(max(n, 0), p.cap) + C::TK - 1) / C::TK;
+            v = ((uint32_t)min(max(n, 0), p.cap) + C::TK - 1) / C::TK;
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -470,10 +483,10 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
         if (b < p.B)
             prefix[b + 1] = v + before;
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0)
         prefix[0] = 0;
-        last_seg[0] = last_seg[1] = -1;
-    }
+    if (threadIdx.x <= kWarps)
+        chains[threadIdx.x].parts = 0;
     if (bad_len && blockIdx.x == 0 && p.status)
         atomicOr(p.status, 2);
     __syncthreads();
@@ -492,58 +505,66 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
                     p.lse[(int64_t)b * Hq + i] = -INFINITY;
         }
 
-    const int64_t total = (int64_t)prefix[p.B] * sh.NS;
-    int64_t want = (total + p.min_tiles - 1) / p.min_tiles;
-    const int nc = (int)min((int64_t)gridDim.x, max(want, (int64_t)1));
-    if ((int)blockIdx.x >= nc || total == 0)
+    const uint32_t total = carry * (uint32_t)sh.NS;
+    // CTAs at work: at least min_tiles tiles each, and few enough for the joins
+    // (splits of an average segment x join_cost <= tiles of a CTA)
+    const uint32_t least = max((float)p.min_tiles, sqrtf((float)carry / p.B * p.join_cost));
+    const uint32_t nc = min(gridDim.x, max(total / least, 1u));
+    if (blockIdx.x >= nc || total == 0)
         return;
-    const int64_t c0 = range_at(total, nc, blockIdx.x), c1 = range_at(total, nc, blockIdx.x + 1);
-    const int64_t w0 = c0 + range_at(c1 - c0, kWarps, warp), w1 = c0 + range_at(c1 - c0, kWarps, warp + 1);
+    const uint32_t c0 = range_at(total, nc, blockIdx.x), c1 = range_at(total, nc, blockIdx.x + 1);
+    const uint32_t w0 = c0 + range_at(c1 - c0, kWarps, warp), w1 = c0 + range_at(c1 - c0, kWarps, warp + 1);
     const float scale2 = p.scale * kLog2e;
 
-    // where the row of query head `r` of segment `seg` goes
-    auto out_row = [&](int b, int seg, int r) -> int {   // query head, or -1 past the group
+    // the query head of row r of a segment, or -1 past the group
+    auto head_of = [&](int seg, int r) -> int {
+        if (p.row_tiles == 1)
+            return r < p.G ? seg * p.G + r : -1;
         const int h = seg / p.row_tiles, i = (seg - h * p.row_tiles) * C::ROWS + r;
         return r < p.rows && i < p.G ? h * p.G + i : -1;
     };
 
     if (w0 < w1) {
-        int left = (int)(w1 - w0), todo = left;   // tiles to issue, tiles to compute
+        uint32_t left = w1 - w0, todo = left;     // tiles to issue, tiles to compute
         Cursor load = cursor_at(sh, w0), cur = load;
+        if (load.tile != 0 && warp == 0 && lane == 0) {
+            const uint32_t end = c0 - load.tile + load.tiles;
+            chains[0] = {0, (int)range_of(c1 - c0, kWarps, min(end, c1) - 1 - c0) + 1, load.b, load.seg, c0 - load.tile, end};
+        }
         bool load_q = true, cur_q = true;         // the segment's query rows come first
         int len = min(p.lens[load.b], p.cap);
+        int64_t head_off = (p.row_tiles == 1 ? load.seg : load.seg / p.row_tiles) * p.head_stride;
         // the next tile's table entries, on the way while earlier tiles are issued: lane i holds key i
         int ent = -1, ent_off = 0;
         auto fetch = [&]() {
-            const int key = load.tile * C::TK + lane;
+            const int key = (int)load.tile * C::TK + lane;
             ent = -1;
             if (lane < C::TK && key < len) {
-                const int blk = key / p.page;
+                const int blk = p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
                 ent_off = key - blk * p.page;
                 ent = p.table[load.b * p.table_stride + blk];
             }
         };
         // Starts the copies of the next item (query rows or a tile) into a stage; the tile's valid keys.
         auto issue = [&](int stage) -> uint32_t {
-            const int h = load.seg / p.row_tiles;
             const uint32_t ks = smem_u32(ring) + stage * 2 * C::TILE_BYTES, vs = ks + C::TILE_BYTES;
             constexpr int EPC = 16 / (int)sizeof(T);                 // elements per chunk
             if (load_q) {
                 load_q = false;
                 for (int i = lane; i < p.rows * C::NCH; i += 32) {
                     const int r = i / C::NCH, ch = i % C::NCH, e = ch * EPC;
-                    const int head = out_row(load.b, load.seg, r);
+                    const int head = head_of(load.seg, r);
                     const bool in = head >= 0 && e < p.D;
                     const T *src = (const T *)p.q + (in ? load.b * p.q_bs + head * p.q_hs + e : 0);
                     cp_async16(ks + r * C::ROW_BYTES + ((ch ^ (r & 7)) << 4), src, in ? 16 : 0);
                 }
                 return 0;
             }
-            bool has = ent >= 0 && ent < p.num_pages;
-            if (!has && lane < C::TK && load.tile * C::TK + lane < len && p.status)
+            const bool has = ent >= 0 && ent < p.num_pages;
+            if (!has && lane < C::TK && (int)load.tile * C::TK + lane < len && p.status)
                 atomicOr(p.status, 1);
             const uint32_t valid = __ballot_sync(0xffffffffu, has);
-            const int64_t off = has ? ent * p.page_stride + ent_off * p.slot_stride + h * p.head_stride : 0;
+            const int64_t off = has ? ent * p.page_stride + ent_off * p.slot_stride + head_off : 0;
             constexpr int RPI = C::NCH >= 32 ? 1 : 32 / C::NCH;      // rows per instruction
             constexpr int CPL = C::NCH > 32 ? C::NCH / 32 : 1;       // chunks of a row per lane
             const int sub = C::NCH >= 32 ? 0 : lane / C::NCH, ch0 = C::NCH >= 32 ? lane : lane % C::NCH;
@@ -566,13 +587,15 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
                 const int b = load.b;
                 advance(sh, load);
                 load_q = load.tile == 0;
+                if (load_q)
+                    head_off = (p.row_tiles == 1 ? load.seg : load.seg / p.row_tiles) * p.head_stride;
                 if (load.b != b)
                     len = min(p.lens[load.b], p.cap);
                 fetch();
             }
             return valid;
         };
-        Acc<C, C::F16> acc;
+        A acc;
         uint32_t vmask[C::STAGES - 1];   // valid keys of the items in flight
         fetch();
 #pragma unroll
@@ -609,16 +632,16 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
                     T *o = (T *)p.out + cur.b * p.o_bs;
                     acc.each(
                         [&](int r, int c, float x, float y, float, float l) {
-                            const int head = out_row(cur.b, cur.seg, r);
+                            const int head = head_of(cur.seg, r);
                             if (head >= 0 && c < p.D) {
                                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                                 store2(o + head * p.o_hs + c, x * inv, y * inv);
                             }
                         },
                         [&](int r, float m, float l) {
-                            const int head = out_row(cur.b, cur.seg, r);
+                            const int head = head_of(cur.seg, r);
                             if (head >= 0 && p.lse)
-                                p.lse[(int64_t)cur.b * Hq + head] = lse_of(m, l * Acc<C, C::F16>::kSumScale);
+                                p.lse[(int64_t)cur.b * Hq + head] = lse_of(m, l * A::kSumScale);
                         });
                 } else {
                     __syncwarp();   // every lane has read the last tile of a ring that is written over
@@ -634,6 +657,11 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
                                 sl[p.rows * p.D + p.rows + r] = l;
                             }
                         });
+                    if (opened && lane == 0) {   // and todo == 0: the segment goes on in the next warp
+                        const uint32_t first = w1 - 1 - cur.tile, end = first + cur.tiles;
+                        chains[1 + warp] = {warp, (int)range_of(c1 - c0, kWarps, min(end, c1) - 1 - c0) - warp + 1,
+                                            cur.b, cur.seg, first, end};
+                    }
                 }
                 opened = true;
                 cur_q = true;
@@ -644,105 +672,149 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
     }
     __syncthreads();
 
-    // Joins n partials: part(i) is the i-th.  All threads of a warp (or of the
-    // CTA, with `tid` and `nt`) take part; sink(r, c, o, l, m) gets each output
-    // before its division by l.
-    auto join = [&](int np, auto part, int tid, int nt, auto sink) {
-        for (int e = tid * 2; e < p.rows * p.D; e += nt * 2) {
-            const int r = e / p.D;
-            float M = -INFINITY;
-            for (int i = 0; i < np; i++)
-                M = fmaxf(M, __ldcg(part(i) + p.rows * p.D + r));
-            const float base = M == -INFINITY ? 0.0f : M;
-            float x = 0.0f, y = 0.0f, l = 0.0f;
-            for (int i = 0; i < np; i++) {
-                const float *q = part(i);
-                const float w = ex2(__ldcg(q + p.rows * p.D + r) - base);
-                const float2 o = __ldcg(reinterpret_cast<const float2 *>(q + e));
-                x = fmaf(w, o.x, x), y = fmaf(w, o.y, y);
-                l = fmaf(w, __ldcg(q + p.rows * p.D + p.rows + r), l);
-            }
-            sink(r, e - r * p.D, x, y, M, l);
-        }
-    };
-    auto write_out = [&](int b, int seg, int r, int c, float x, float y, float M, float l) {
-        const int head = out_row(b, seg, r);
-        if (head < 0)
-            return;
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        store2((T *)p.out + b * p.o_bs + head * p.o_hs + c, x * inv, y * inv);
-        if (c == 0 && p.lse)
-            p.lse[(int64_t)b * Hq + head] = lse_of(M, l * Acc<C, C::F16>::kSumScale);
+    auto write4 = [&](int b, int head, int c, float4 o, float inv) {
+        T *d = (T *)p.out + b * p.o_bs + head * p.o_hs + c;
+        store2(d, o.x * inv, o.y * inv);
+        store2(d + 2, o.z * inv, o.w * inv);
     };
 
-    // segments that cross warps: the one that the CTA's range begins inside of
-    // (warp 0), and the one whose first tile is in this warp but not its last
-    for (int kind = 0; kind < 2; kind++) {
-        if (w0 >= w1 || (kind == 0 && warp != 0))
+    // segments that cross warps: finished here, or this CTA's part of them to the workspace
+    const int n4 = p.rows * p.D / 4;
+    bool wrote = false;
+    for (int k = 0; k <= kWarps; k++) {
+        const Chain ch = chains[k];
+        if (ch.parts == 0)
             continue;
-        const Cursor cu = cursor_at(sh, kind == 0 ? c0 : w1 - 1);
-        const int64_t at = kind == 0 ? c0 : w1 - 1;
-        const int64_t first = at - cu.tile, end = first + cu.tiles;   // the segment's tiles
-        if (kind == 0 ? cu.tile == 0 : (first < w0 || end <= w1))
-            continue;
-        const int64_t stop = min(end, c1);
-        const int wl = range_of(c1 - c0, kWarps, stop - 1 - c0);
-        const bool whole = first >= c0 && end <= c1;
-        float *dst = p.partials + ((int64_t)blockIdx.x * 2 + kind) * pf;
-        auto part = [&](int i) -> const float * { return slot_of(warp + i, kind == 1 && i == 0); };
-        const int np = wl - warp + 1;
-        for (int e = lane * 2; e < p.rows * p.D; e += 64) {
-            const int r = e / p.D;
-            float M = -INFINITY;
-            for (int i = 0; i < np; i++)
-                M = fmaxf(M, part(i)[p.rows * p.D + r]);
-            const float base = M == -INFINITY ? 0.0f : M;
-            float x = 0.0f, y = 0.0f, l = 0.0f;
-            for (int i = 0; i < np; i++) {
-                const float *q = part(i);
-                const float w = ex2(q[p.rows * p.D + r] - base);
-                const float2 o = *reinterpret_cast<const float2 *>(q + e);
-                x = fmaf(w, o.x, x), y = fmaf(w, o.y, y), l = fmaf(w, q[p.rows * p.D + p.rows + r], l);
+        const bool whole = ch.first >= c0 && ch.end <= c1;
+        float *dst = p.partials + ((int64_t)blockIdx.x * 2 + (k > 0)) * pf;
+        wrote |= !whole;
+        for (int i = threadIdx.x; i < n4; i += kThreads) {
+            const int r = i * 4 / p.D, c = i * 4 - r * p.D;
+            float m[kWarps], M = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kWarps; j++) {
+                m[j] = j < ch.parts ? slot_of(ch.warp + j, k > 0 && j == 0)[p.rows * p.D + r] : -INFINITY;
+                M = fmaxf(M, m[j]);
             }
+            const float base = M == -INFINITY ? 0.0f : M;
+            float4 o = make_float4(0, 0, 0, 0);
+            float l = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kWarps; j++)
+                if (j < ch.parts) {
+                    const float *part = slot_of(ch.warp + j, k > 0 && j == 0);
+                    const float w = ex2(m[j] - base);
+                    fma4(o, w, *reinterpret_cast<const float4 *>(part + i * 4));
+                    l = fmaf(w, part[p.rows * p.D + p.rows + r], l);
+                }
             if (whole) {
-                write_out(cu.b, cu.seg, r, e - r * p.D, x, y, M, l);
+                const int head = head_of(ch.seg, r);
+                if (head >= 0) {
+                    write4(ch.b, head, c, o, l > 0.0f ? 1.0f / l : 0.0f);
+                    if (c == 0 && p.lse)
+                        p.lse[(int64_t)ch.b * Hq + head] = lse_of(M, l * A::kSumScale);
+                }
             } else {
-                *reinterpret_cast<float2 *>(dst + e) = make_float2(x, y);
-                if (e == r * p.D) {
+                *reinterpret_cast<float4 *>(dst + i * 4) = o;
+                if (c == 0) {
                     dst[p.rows * p.D + r] = M;
                     dst[p.rows * p.D + p.rows + r] = l;
                 }
             }
         }
-        if (!whole) {
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) {
-                const int cf = range_of(total, nc, first), cl = range_of(total, nc, end - 1);
-                const int id = cu.b * sh.NS + cu.seg;
-                if (atomicAdd(p.counters + cf, 1) == cl - cf) {
-                    p.counters[cf] = 0;
-                    last_seg[kind] = id;
-                }
+    }
+    if (!wrote)   // the same in every thread
+        return;
+
+    // segments that cross CTAs: the CTA that arrives last joins the parts, in CTA order
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        int mine = -1;
+        for (int k = threadIdx.x; k <= (threadIdx.x ? kWarps : 0); k++) {
+            const Chain &ch = chains[k];
+            if (ch.parts == 0 || (ch.first >= c0 && ch.end <= c1))
+                continue;
+            const uint32_t cf = range_of(total, nc, ch.first), cl = range_of(total, nc, ch.end - 1);
+            if ((uint32_t)atomicAdd(p.counters + cf, 1) == cl - cf) {
+                p.counters[cf] = 0;
+                mine = k;
             }
         }
+        last[threadIdx.x] = mine;
     }
     __syncthreads();
-
-    // segments that cross CTAs and whose last part was written here
+    float *wm = reinterpret_cast<float *>(smem);   // the rings are free now; the host bounds nc so that this fits them
     for (int kind = 0; kind < 2; kind++) {
-        const int id = last_seg[kind];
-        if (id < 0)
+        if (last[kind] < 0)
             continue;
         __threadfence();
-        const int b = id / sh.NS, seg = id - b * sh.NS;
-        const int tiles = (int)(prefix[b + 1] - prefix[b]);
-        const int64_t first = (int64_t)prefix[b] * sh.NS + (int64_t)seg * tiles;
-        const int cf = range_of(total, nc, first), cl = range_of(total, nc, first + tiles - 1);
-        auto part = [&](int i) -> const float * { return p.partials + ((int64_t)(cf + i) * 2 + (i == 0 ? 1 : 0)) * pf; };
-        join(cl - cf + 1, part, threadIdx.x, kThreads, [&](int r, int c, float x, float y, float M, float l) {
-            write_out(b, seg, r, c, x, y, M, l);
-        });
+        const Chain ch = chains[last[kind]];
+        const int cf = (int)range_of(total, nc, ch.first), np = (int)range_of(total, nc, ch.end - 1) - cf + 1;
+        const float *first = p.partials + ((int64_t)cf * 2 + 1) * pf;             // part 0; part i at rest + (i - 1) * 2 pf
+        const float *rest = p.partials + ((int64_t)cf + 1) * 2 * pf;
+        auto part = [&](int i) { return i == 0 ? first : rest + (int64_t)(i - 1) * 2 * pf; };
+        // weights exp2(m_i - M) / sum, per row: [row][np]
+        float *wl = wm + p.rows * np, *red = wm + (2 * p.rows * np + 3) / 4 * 4;
+        for (int i = threadIdx.x; i < np * p.rows; i += kThreads) {
+            const int pi = i / p.rows, r = i - pi * p.rows;
+            const float *q = part(pi) + p.rows * p.D;
+            wm[r * np + pi] = __ldcg(q + r);
+            wl[r * np + pi] = __ldcg(q + p.rows + r);
+        }
+        __syncthreads();
+        for (int r = warp; r < p.rows; r += kWarps) {
+            float M = -INFINITY, l = 0.0f;
+            for (int i = lane; i < np; i += 32)
+                M = fmaxf(M, wm[r * np + i]);
+#pragma unroll
+            for (int x = 16; x; x >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+            const float base = M == -INFINITY ? 0.0f : M;
+            for (int i = lane; i < np; i += 32) {
+                const float w = ex2(wm[r * np + i] - base);
+                wm[r * np + i] = w;
+                l = fmaf(w, wl[r * np + i], l);
+            }
+#pragma unroll
+            for (int x = 16; x; x >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, x);
+            __syncwarp();
+            const int head = head_of(ch.seg, r);
+            if (lane == 0) {
+                wl[r * np] = l > 0.0f ? 1.0f / l : 0.0f;
+                if (head >= 0 && p.lse)
+                    p.lse[(int64_t)ch.b * Hq + head] = lse_of(M, l * A::kSumScale);
+            }
+        }
+        __syncthreads();
+        // few outputs: `groups` sets of threads take every groups-th part each
+        int groups = 1;
+        while (groups < 8 && n4 * groups * 2 <= kThreads)
+            groups *= 2;
+        const int g = threadIdx.x / (kThreads / groups);
+        for (int i0 = 0; i0 < n4; i0 += kThreads / groups) {
+            const int i = i0 + (int)threadIdx.x % (kThreads / groups);
+            float4 o = make_float4(0, 0, 0, 0);
+            const int r = i * 4 / p.D, c = i * 4 - r * p.D;
+            if (i < n4) {
+#pragma unroll 8
+                for (int j = g; j < np; j += groups)
+                    fma4(o, wm[r * np + j], __ldcg(reinterpret_cast<const float4 *>(part(j) + i * 4)));
+            }
+            if (groups > 1) {   // n4 <= kThreads / groups: one round
+                if (g > 0 && i < n4)
+                    *reinterpret_cast<float4 *>(red + (g * n4 + i) * 4) = o;
+                __syncthreads();
+                if (g == 0 && i < n4)
+                    for (int x = 1; x < groups; x++)
+                        fma4(o, 1.0f, *reinterpret_cast<const float4 *>(red + (x * n4 + i) * 4));
+            }
+            const int head = g == 0 && i < n4 ? head_of(ch.seg, r) : -1;
+            if (head >= 0)
+                write4(ch.b, head, c, o, wl[r * np]);
+        }
+        __syncthreads();
     }
 }
 
@@ -752,7 +824,10 @@ constexpr size_t kSmemTwo = 113 * 1024 - 256;   // two CTAs on an SM
 template <typename C>
 int launch_cfg(const AttnParams &p, int most, size_t smem, unsigned flags, cudaStream_t s) {
     const int resident = device_sm_count() * (smem <= kSmemTwo ? 2 : 1);
-    const int grid = most < resident ? most : resident;
+    // the last join keeps two floats per row and part, and 16 bytes per thread, in the rings
+    const int joinable = (kWarps * C::STAGES * 2 * C::TILE_BYTES - kThreads * 16 - 16) / (8 * p.rows);
+    int grid = most < resident ? most : resident;
+    grid = grid < joinable ? grid : joinable;
     static int cache[kMaxDevices] = {};
     auto *kernel = paged_attention_kernel<C>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)smem, cache);
@@ -829,12 +904,18 @@ int launch_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_
     p.rows = rows_per_segment(p.G, f16);
     p.row_tiles = (p.G + p.rows - 1) / p.rows;
     p.page = (int)c->page_size, p.num_pages = (int)c->num_pages, p.cap = max_blocks * p.page, p.scale = scale;
+    p.page_shift = (p.page & (p.page - 1)) == 0 ? __builtin_ctz((unsigned)p.page) : -1;
     p.min_tiles = kWarps;
+    p.join_cost = (float)(p.rows * (p.D + 2) * 4) / (2 * (f16 ? 16 * 2 : 8 * 4) * p.D);   // bytes over bytes
     p.counters = (int *)workspace;
     p.partials = (float *)((uint8_t *)workspace + counters_bytes());
     // no more CTAs than the table's width could need
     const int tk = f16 ? 16 : 8;
-    const int64_t most = ((int64_t)B * ((p.cap + tk - 1) / tk) * p.Hkv * p.row_tiles + p.min_tiles - 1) / p.min_tiles;
+    const int64_t tiles = (int64_t)B * ((p.cap - 1) / tk + 1) * p.Hkv * p.row_tiles;
+    if (tiles > 0x7fffffff)
+        return fail(MNB_ERR_SHAPE, "mnb_paged_attention: B=%d requests of up to %d tokens in %d heads are 2^31 tiles or more",
+                    B, p.cap, p.Hkv * p.row_tiles);
+    const int64_t most = (tiles + p.min_tiles - 1) / p.min_tiles;
     const int ctas = (int)(most < grid_of() ? (most < 1 ? 1 : most) : grid_of());
     if (f16)
         return p.D <= 64    ? launch_dp<half, 64>(p, ctas, flags, s)
