@@ -382,7 +382,8 @@ typedef struct mnb_paged_cache {
     int64_t page_size;      /* tokens per page, any positive number */
     int64_t num_heads;      /* KV heads */
     int64_t head_dim;       /* entries of a head, contiguous; a multiple of 8, <= 256 */
-    int64_t page_stride, slot_stride, head_stride;   /* elements, the same for k and v; multiples of 16 bytes */
+    int64_t page_stride, slot_stride, head_stride;   /* elements, the same for k and v; multiples of 16 bytes
+                                                        (strides of a single extent mean nothing) */
     int32_t dtype;          /* MNB_F16 or MNB_F32: of the cache and of q, k, v and out */
     int32_t reserved;       /* 0 */
 } mnb_paged_cache;

@@ -14,7 +14,9 @@ nibble of byte j), scales fp32/fp16 [N, K/bs], zero points uint8
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 
 import torch
 
@@ -93,10 +95,10 @@ def _load():
         "mnb_gptq_quantize": ([vp, vp, vp, i64, i64, i32, i32, vp, vp, i32, vp, vp], i32),
         "mnb_paged_tables": ([vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, i64, vp, vp, u32, vp],
                              i32),
-        "mnb_rope_append": ([vp, i64, i64, vp, i64, i64, vp, i64, i64, P(mnb_paged_cache), vp, vp, i64, i64, vp, vp,
+        "mnb_rope_append": ([vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp, i64, i64, vp, vp,
                              i64, i64, vp, vp, ctypes.c_float, vp, i64, i64, vp, u32, vp], i32),
         "mnb_paged_attention_workspace_bytes": ([i64, i64, i64, i64, i32], sz),
-        "mnb_paged_attention": ([vp, i64, i64, P(mnb_paged_cache), vp, i64, i64, vp, i64, i64, ctypes.c_float, vp,
+        "mnb_paged_attention": ([vp, i64, i64, vp, vp, i64, i64, vp, i64, i64, ctypes.c_float, vp,
                                  i64, i64, vp, vp, sz, vp, u32, vp], i32),
     }
     for name, (args, res) in sig.items():
@@ -124,9 +126,14 @@ def _dt(t):
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -314,66 +321,44 @@ def mnb_gptq_quantize(W, U, dead, bs, has_zp, packed, scales, zp, stream=None):
 
 
 
-def _device_tensors(fn, dtype, **ts):
-    """Each given tensor (None passes) is of `dtype` (None: any) and on the current CUDA device."""
-    for name, t in ts.items():
+# ---- paged key-value cache.  A decode step makes these calls once per layer, so
+# the checks that pass read each property of a tensor once and call no helper
+# per tensor; what a failed one has found is worked out afterwards, in _explain.
+
+_pack_cache = struct.Struct("@PPqqqqqqqii").pack   # mnb_paged_cache as bytes
+_PAGED_DT = {torch.float16: MNB_F16, torch.float32: MNB_F32}
+
+
+def _explain(fn, **ts):
+    """Raises for the first tensor that is not as described: (tensor, dtype, shape, layout).  layout "flat":
+    contiguous, as many elements as the shape has; "rows": that shape, a contiguous last dimension; "same": the
+    strides of k_cache besides."""
+    for name, (t, dtype, shape, layout) in ts.items():
         if t is None:
             continue
-        if dtype is not None and t.dtype != dtype:
+        if t.dtype != dtype:
             raise MnbError(fn, -1, f"{name} is {t.dtype}, not {dtype}")
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        if tuple(t.shape) != shape and (layout != "flat" or t.numel() != math.prod(shape)):
+            raise MnbError(fn, -2, f"{name} has shape {tuple(t.shape)}, not {shape}")
+        if layout == "flat" and not t.is_contiguous():
+            raise MnbError(fn, -1, f"{name} must be contiguous")
+        if layout != "flat" and t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+            raise MnbError(fn, -1, f"{name}'s last dimension must be contiguous")
+        if layout == "same" and t.stride() != ts["k_cache"][0].stride():
+            raise MnbError(fn, -1, f"{name} must have k_cache's strides")
+    for name, (t, *_) in ts.items():
+        if t is not None and (not t.is_cuda or t.get_device() != torch.cuda.current_device()):
             raise MnbError(fn, -1, f"{name} is on {t.device}, not on the current CUDA device")
+    raise MnbError(fn, -1, "arguments do not fit together")
 
 
-def _shaped(fn, name, t, *shape):
-    if tuple(t.shape) != shape:
-        raise MnbError(fn, -2, f"{name} has shape {tuple(t.shape)}, not {shape}")
-
-
-def _vectors(fn, n, **ts):
-    for name, t in ts.items():
-        if t is not None:
-            _shaped(fn, name, t, n)
-            if not t.is_contiguous():
-                raise MnbError(fn, -1, f"{name} must be contiguous")
-
-
-def _status_word(fn, status):
-    _device_tensors(fn, torch.int32, status=status)
-    if status is not None and status.numel() != 1:
-        raise MnbError(fn, -2, "status must have one element")
-
-
-def _rows(fn, name, t, n, heads, D):
-    """(pointer, row stride, head stride) of t [n, heads, D] with contiguous heads."""
-    if t is None:
-        return None, 0, 0
-    _shaped(fn, name, t, n, heads, D)
-    if D > 1 and t.stride(2) != 1:
-        raise MnbError(fn, -1, f"{name}'s last dimension must be contiguous")
-    return _ptr(t), t.stride(0) if n > 1 else 0, t.stride(1) if heads > 1 else 0
-
-
-def _paged_cache(fn, k_cache, v_cache):
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise MnbError(fn, -2, "k_cache and v_cache must have one shape [pages, page_size, heads, head size]")
-    if v_cache.dtype != k_cache.dtype or k_cache.dtype not in (torch.float16, torch.float32):
-        raise MnbError(fn, -1, f"k_cache is {k_cache.dtype}, v_cache {v_cache.dtype}: fp16 or fp32, the same")
-    _device_tensors(fn, k_cache.dtype, k_cache=k_cache, v_cache=v_cache)
-    P, ps, H, D = k_cache.shape
-    strides = [st if n > 1 else 0 for st, n in zip(k_cache.stride(), k_cache.shape)]
-    if strides != [st if n > 1 else 0 for st, n in zip(v_cache.stride(), v_cache.shape)] or (D > 1 and strides[3] != 1):
-        raise MnbError(fn, -1, "k_cache and v_cache must have the same strides, the last dimension contiguous")
-    return mnb_paged_cache(_ptr(k_cache), _ptr(v_cache), P, ps, H, D, strides[0], strides[1], strides[2],
-                           _dt(k_cache), 0)
-
-
-def _block_table(fn, block_table, B):
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise MnbError(fn, -2, f"block_table has shape {tuple(block_table.shape)}, not [{B}, blocks]")
-    if B > 0 and block_table.shape[1] > 1 and block_table.stride(1) != 1:
-        raise MnbError(fn, -1, "block_table's rows must be contiguous")
-    return block_table.stride(0) if B > 1 else block_table.shape[1]
+def _pool_dtype(fn, k_cache):
+    dt = _PAGED_DT.get(k_cache.dtype)
+    if dt is None:
+        raise MnbError(fn, -1, f"k_cache is {k_cache.dtype}: fp16 or fp32")
+    if k_cache.dim() != 4:
+        raise MnbError(fn, -2, f"k_cache has shape {tuple(k_cache.shape)}, not [pages, page_size, heads, head size]")
+    return dt
 
 
 def mnb_paged_tables(ctx_lens, new_lens, block_table, page_size, num_pages, free_pages, free_start, seq_lens, cu_new,
@@ -381,22 +366,41 @@ def mnb_paged_tables(ctx_lens, new_lens, block_table, page_size, num_pages, free
     """Pages for new_lens [B] more tokens behind ctx_lens [B]: taken from free_pages [F], at free_start [1] and on,
     into block_table [B, blocks]; seq_lens [B], cu_new [B + 1], slots and positions [T] of the new tokens (-1 and 0
     behind the last), free_next [1].  All int32."""
-    fn = "mnb_paged_tables"
-    _device_tensors(fn, torch.int32, ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table,
-                    free_pages=free_pages, free_start=free_start, seq_lens=seq_lens, cu_new=cu_new, slots=slots,
-                    positions=positions, free_next=free_next)
-    _status_word(fn, status)
-    B, T = ctx_lens.numel(), slots.numel()
-    _vectors(fn, B, ctx_lens=ctx_lens, new_lens=new_lens, seq_lens=seq_lens)
-    _vectors(fn, B + 1, cu_new=cu_new)
-    _vectors(fn, T, slots=slots, positions=positions)
-    _vectors(fn, 1, free_start=free_start, free_next=free_next)
-    _vectors(fn, free_pages.numel(), free_pages=free_pages)
-    stride = _block_table(fn, block_table, B)
-    _check(fn, _lib.mnb_paged_tables(
-        _ptr(ctx_lens), _ptr(new_lens), B, page_size, num_pages, _ptr(free_pages), free_pages.numel(),
-        _ptr(free_start), _ptr(block_table), stride, block_table.shape[1], _ptr(seq_lens), _ptr(cu_new), _ptr(slots),
-        _ptr(positions), T, _ptr(free_next), _ptr(status), flags, _stream(stream)))
+    fn, i32 = "mnb_paged_tables", torch.int32
+    dev = ctx_lens.get_device()
+    B, T, F = ctx_lens.numel(), slots.numel(), free_pages.numel()
+    rows, blocks = block_table.shape if block_table.dim() == 2 else (-1, -1)
+    stride, last = block_table.stride() if rows >= 0 else (0, 0)
+    if not (dev >= 0 and dev == torch.cuda.current_device() and
+            ctx_lens.dtype is i32 and ctx_lens.is_contiguous() and
+            new_lens.dtype is i32 and new_lens.numel() == B and new_lens.is_contiguous() and
+            new_lens.get_device() == dev and
+            free_pages.dtype is i32 and free_pages.is_contiguous() and free_pages.get_device() == dev and
+            free_start.dtype is i32 and free_start.numel() == 1 and free_start.get_device() == dev and
+            free_next.dtype is i32 and free_next.numel() == 1 and free_next.get_device() == dev and
+            seq_lens.dtype is i32 and seq_lens.numel() == B and seq_lens.is_contiguous() and
+            seq_lens.get_device() == dev and
+            cu_new.dtype is i32 and cu_new.numel() == B + 1 and cu_new.is_contiguous() and
+            cu_new.get_device() == dev and
+            slots.dtype is i32 and slots.is_contiguous() and slots.get_device() == dev and
+            positions.dtype is i32 and positions.numel() == T and positions.is_contiguous() and
+            positions.get_device() == dev and
+            block_table.dtype is i32 and rows == B and (last == 1 or blocks == 1 or B == 0) and
+            block_table.get_device() == dev and
+            (status is None or (status.dtype is i32 and status.numel() == 1 and status.get_device() == dev))):
+        _explain(fn, ctx_lens=(ctx_lens, i32, (B,), "flat"), new_lens=(new_lens, i32, (B,), "flat"),
+                 block_table=(block_table, i32, (B, blocks), "rows"), free_pages=(free_pages, i32, (F,), "flat"),
+                 free_start=(free_start, i32, (1,), "flat"), seq_lens=(seq_lens, i32, (B,), "flat"),
+                 cu_new=(cu_new, i32, (B + 1,), "flat"), slots=(slots, i32, (T,), "flat"),
+                 positions=(positions, i32, (T,), "flat"), free_next=(free_next, i32, (1,), "flat"),
+                 status=(status, i32, (1,), "flat"))
+    rc = _lib.mnb_paged_tables(
+        ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size, num_pages, free_pages.data_ptr(), F,
+        free_start.data_ptr(), block_table.data_ptr(), stride if B > 1 else blocks, blocks, seq_lens.data_ptr(),
+        cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(), T, free_next.data_ptr(),
+        None if status is None else status.data_ptr(), flags, _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(fn, rc)
 
 
 def mnb_rope_append(q, k, v, k_cache, v_cache, slots, positions, cos, sin, q_out, q_weight=None, k_weight=None,
@@ -404,37 +408,72 @@ def mnb_rope_append(q, k, v, k_cache, v_cache, slots, positions, cos, sin, q_out
     """RMS norm (where a weight [D] is given) and rotary embedding (unless cos is None) of q [T, Hq, D] into q_out and
     of k [T, Hkv, D] into rows slots [T] of k_cache [pages, page_size, Hkv, D]; v likewise, as it is, into v_cache.
     cos, sin: fp32 [positions, rot_dim / 2].  q and q_out may be None (keys and values alone), or one tensor."""
-    fn = "mnb_rope_append"
-    if (q is None) != (q_out is None):
-        raise MnbError(fn, -1, "q and q_out go together")
-    if (cos is None) != (sin is None):
-        raise MnbError(fn, -1, "cos and sin go together")
-    if cos is not None and positions is None:
-        raise MnbError(fn, -1, "a rotation needs positions")
-    cache = _paged_cache(fn, k_cache, v_cache)
-    H, D = k_cache.shape[2:]
-    T, Hq = slots.numel(), 0 if q is None else q.shape[1] if q.dim() == 3 else -1
-    _device_tensors(fn, k_cache.dtype, q=q, k=k, v=v, q_out=q_out)
-    _device_tensors(fn, torch.float32, cos=cos, sin=sin, q_weight=q_weight, k_weight=k_weight)
-    _device_tensors(fn, torch.int32, slots=slots, positions=positions)
-    _status_word(fn, status)
-    _vectors(fn, T, slots=slots, positions=positions)
-    _vectors(fn, D, q_weight=q_weight, k_weight=k_weight)
-    R = num_pos = 0
+    fn, f32, i32, dtype = "mnb_rope_append", torch.float32, torch.int32, k_cache.dtype
+    if (q is None) != (q_out is None) or (cos is None) != (sin is None) or (cos is not None and positions is None):
+        raise MnbError(fn, -1, "q and q_out go together, and cos, sin and positions")
+    dt, dev = _pool_dtype(fn, k_cache), k_cache.get_device()
+    shape, strides = k_cache.shape, k_cache.stride()
+    P, ps, H, D = shape
+    T = slots.numel()
+    rows = (T, H, D)
+    ks = vs = qs = os_ = (0, 0, 1)
+    ok = (dev >= 0 and dev == torch.cuda.current_device() and
+          v_cache.shape == shape and v_cache.dtype is dtype and v_cache.get_device() == dev and
+          v_cache.stride() == strides and (strides[3] == 1 or D == 1) and
+          k.shape == rows and k.dtype is dtype and k.get_device() == dev and
+          v.shape == rows and v.dtype is dtype and v.get_device() == dev and
+          slots.dtype is i32 and slots.is_contiguous() and slots.get_device() == dev and
+          (status is None or (status.dtype is i32 and status.numel() == 1 and status.get_device() == dev)))
+    if ok:
+        ks, vs = k.stride(), v.stride()
+        ok = (ks[2] == 1 and vs[2] == 1) or T * D <= 1
+    Hq = half = num_pos = 0
+    qp = op = cp = sp = pp = qwp = kwp = None
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else -1
+        rows = (T, Hq, D)
+        ok = (ok and q.shape == rows and q.dtype is dtype and q.get_device() == dev and
+              q_out.shape == rows and q_out.dtype is dtype and q_out.get_device() == dev)
+        if ok:
+            qs, os_ = q.stride(), q_out.stride()
+            ok = (qs[2] == 1 and os_[2] == 1) or T * D <= 1
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    if positions is not None:
+        ok = (ok and positions.dtype is i32 and positions.numel() == T and positions.is_contiguous() and
+              positions.get_device() == dev)
+        pp = positions.data_ptr()
     if cos is not None:
-        if cos.dim() != 2 or sin.shape != cos.shape:
-            raise MnbError(fn, -2, "cos and sin must have one shape [positions, rot_dim / 2]")
-        _contiguous(fn, cos, sin)
-        num_pos, R = cos.shape[0], 2 * cos.shape[1]
-    _check(fn, _lib.mnb_rope_append(
-        *_rows(fn, "q", q, T, Hq, D), *_rows(fn, "k", k, T, H, D), *_rows(fn, "v", v, T, H, D), ctypes.byref(cache),
-        _ptr(slots), _ptr(positions), T, Hq, _ptr(cos), _ptr(sin), R, num_pos, _ptr(q_weight), _ptr(k_weight), eps,
-        *_rows(fn, "q_out", q_out, T, Hq, D), _ptr(status), flags, _stream(stream)))
+        num_pos, half = cos.shape if cos.dim() == 2 else (-1, 0)
+        ok = (ok and cos.dtype is f32 and cos.is_contiguous() and cos.get_device() == dev and num_pos >= 0 and
+              sin.dtype is f32 and sin.shape == cos.shape and sin.is_contiguous() and sin.get_device() == dev)
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    if q_weight is not None:
+        ok = (ok and q_weight.dtype is f32 and q_weight.numel() == D and q_weight.is_contiguous() and
+              q_weight.get_device() == dev)
+        qwp = q_weight.data_ptr()
+    if k_weight is not None:
+        ok = (ok and k_weight.dtype is f32 and k_weight.numel() == D and k_weight.is_contiguous() and
+              k_weight.get_device() == dev)
+        kwp = k_weight.data_ptr()
+    if not ok:
+        _explain(fn, k_cache=(k_cache, dtype, tuple(shape), "rows"), v_cache=(v_cache, dtype, tuple(shape), "same"),
+                 q=(q, dtype, (T, Hq, D), "rows"), k=(k, dtype, (T, H, D), "rows"), v=(v, dtype, (T, H, D), "rows"),
+                 q_out=(q_out, dtype, (T, Hq, D), "rows"), slots=(slots, i32, (T,), "flat"),
+                 positions=(positions, i32, (T,), "flat"), cos=(cos, f32, (num_pos, half), "flat"),
+                 sin=(sin, f32, (num_pos, half), "flat"), q_weight=(q_weight, f32, (D,), "flat"),
+                 k_weight=(k_weight, f32, (D,), "flat"), status=(status, i32, (1,), "flat"))
+    cache = _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), P, ps, H, D, strides[0], strides[1], strides[2], dt, 0)
+    rc = _lib.mnb_rope_append(
+        qp, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], cache, slots.data_ptr(), pp, T, Hq,
+        cp, sp, 2 * half, num_pos, qwp, kwp, eps, op, os_[0], os_[1], None if status is None else status.data_ptr(),
+        flags, _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(fn, rc)
 
 
 def mnb_paged_attention_workspace_bytes(B, Hq, Hkv, D, dtype=torch.float16) -> int:
     """Bytes of (zero-filled) workspace of mnb_paged_attention on the current device."""
-    return _lib.mnb_paged_attention_workspace_bytes(B, Hq, Hkv, D, MNB_F16 if dtype == torch.float16 else MNB_F32)
+    return _lib.mnb_paged_attention_workspace_bytes(B, Hq, Hkv, D, _PAGED_DT.get(dtype, -1))
 
 
 def mnb_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, workspace, lse=None, status=None,
@@ -442,23 +481,42 @@ def mnb_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, 
     """out [B, Hq, D] = softmax(scale * q k^T) v of one token per request over the first seq_lens [B] rows of its
     pages block_table [B, blocks] of k_cache, v_cache [pages, page_size, Hkv, D]; lse fp32 [B, Hq].
     workspace: a zero-filled uint8 tensor of mnb_paged_attention_workspace_bytes bytes."""
-    fn = "mnb_paged_attention"
-    cache = _paged_cache(fn, k_cache, v_cache)
-    D = k_cache.shape[3]
-    if q.dim() != 3:
-        raise MnbError(fn, -2, f"q has shape {tuple(q.shape)}, not [requests, heads, head size]")
-    B, Hq = q.shape[:2]
-    _device_tensors(fn, k_cache.dtype, q=q, out=out)
-    _device_tensors(fn, torch.int32, block_table=block_table, seq_lens=seq_lens)
-    _device_tensors(fn, torch.float32, lse=lse)
-    _device_tensors(fn, None, workspace=workspace)
-    _status_word(fn, status)
-    _vectors(fn, B, seq_lens=seq_lens)
-    if lse is not None:
-        _shaped(fn, "lse", lse, B, Hq)
-    _contiguous(fn, lse, workspace)
-    stride = _block_table(fn, block_table, B)
-    _check(fn, _lib.mnb_paged_attention(
-        *_rows(fn, "q", q, B, Hq, D), ctypes.byref(cache), _ptr(block_table), stride, block_table.shape[1],
-        _ptr(seq_lens), B, Hq, scale, *_rows(fn, "out", out, B, Hq, D), _ptr(lse), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(status), flags, _stream(stream)))
+    fn, i32, dtype = "mnb_paged_attention", torch.int32, k_cache.dtype
+    dt, dev = _pool_dtype(fn, k_cache), k_cache.get_device()
+    shape, strides = k_cache.shape, k_cache.stride()
+    P, ps, H, D = shape
+    B, Hq, _ = q.shape if q.dim() == 3 else (seq_lens.numel(), -1, D)
+    rows = (B, Hq, D)
+    table_rows, blocks = block_table.shape if block_table.dim() == 2 else (-1, -1)
+    table_stride, last = block_table.stride() if table_rows >= 0 else (0, 0)
+    qs = os_ = (0, 0, 1)
+    ok = (dev >= 0 and dev == torch.cuda.current_device() and
+          v_cache.shape == shape and v_cache.dtype is dtype and v_cache.get_device() == dev and
+          v_cache.stride() == strides and (strides[3] == 1 or D == 1) and
+          q.shape == rows and q.dtype is dtype and q.get_device() == dev and
+          out.shape == rows and out.dtype is dtype and out.get_device() == dev and
+          block_table.dtype is i32 and table_rows == B and (last == 1 or blocks == 1 or B == 0) and
+          block_table.get_device() == dev and
+          seq_lens.dtype is i32 and seq_lens.numel() == B and seq_lens.is_contiguous() and
+          seq_lens.get_device() == dev and
+          workspace.dtype is torch.uint8 and workspace.is_contiguous() and workspace.get_device() == dev and
+          (lse is None or (lse.dtype is torch.float32 and lse.numel() == B * Hq and lse.is_contiguous() and
+                           lse.get_device() == dev)) and
+          (status is None or (status.dtype is i32 and status.numel() == 1 and status.get_device() == dev)))
+    if ok:
+        qs, os_ = q.stride(), out.stride()
+        ok = (qs[2] == 1 and os_[2] == 1) or B * D <= 1
+    if not ok:
+        _explain(fn, k_cache=(k_cache, dtype, tuple(shape), "rows"), v_cache=(v_cache, dtype, tuple(shape), "same"),
+                 q=(q, dtype, rows, "rows"), out=(out, dtype, rows, "rows"),
+                 block_table=(block_table, i32, (B, blocks), "rows"), seq_lens=(seq_lens, i32, (B,), "flat"),
+                 workspace=(workspace, torch.uint8, (workspace.numel(),), "flat"),
+                 lse=(lse, torch.float32, (B, Hq), "flat"), status=(status, i32, (1,), "flat"))
+    cache = _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), P, ps, H, D, strides[0], strides[1], strides[2], dt, 0)
+    rc = _lib.mnb_paged_attention(
+        q.data_ptr(), qs[0], qs[1], cache, block_table.data_ptr(), table_stride if B > 1 else blocks, blocks,
+        seq_lens.data_ptr(), B, Hq, scale, out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), None if status is None else status.data_ptr(), flags,
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check(fn, rc)

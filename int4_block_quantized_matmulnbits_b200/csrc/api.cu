@@ -134,9 +134,19 @@ static int check_stride(const char *fn, int64_t stride, int dtype) {
     return MNB_OK;
 }
 
-static int check_paged_cache(const char *fn, const mnb_paged_cache *c) {
+// Checks *given and copies it to *c, the strides of single extents as 0.
+static int check_paged_cache(const char *fn, const mnb_paged_cache *given, mnb_paged_cache *c) {
     int rc;
-    if (!c || !c->k || !c->v)
+    if (!given)
+        return fail(MNB_ERR_INVALID_ARG, "%s: NULL cache", fn);
+    *c = *given;
+    if (c->num_pages == 1)
+        c->page_stride = 0;
+    if (c->page_size == 1)
+        c->slot_stride = 0;
+    if (c->num_heads == 1)
+        c->head_stride = 0;
+    if (!c->k || !c->v)
         return fail(MNB_ERR_INVALID_ARG, "%s: NULL cache", fn);
     if ((rc = check_dtype(fn, "cache", c->dtype)))
         return rc;
@@ -538,13 +548,14 @@ int mnb_paged_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B
 }
 
 int mnb_rope_append(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs,
-                    const void *v, int64_t v_ts, int64_t v_hs, const mnb_paged_cache *cache, const int32_t *slots,
+                    const void *v, int64_t v_ts, int64_t v_hs, const mnb_paged_cache *given, const int32_t *slots,
                     const int32_t *positions, int64_t T, int64_t Hq, const float *cos, const float *sin,
                     int64_t rot_dim, int64_t num_pos, const float *q_weight, const float *k_weight, float eps,
                     void *q_out, int64_t o_ts, int64_t o_hs, int *status, unsigned flags, void *stream) {
     clear_error();
     const char *fn = "mnb_rope_append";
-    int rc = check_paged_cache(fn, cache);
+    mnb_paged_cache pool, *cache = &pool;
+    int rc = check_paged_cache(fn, given, cache);
     if (rc)
         return rc;
     if (T < 0 || Hq < 0 || rot_dim < 0)
@@ -571,6 +582,14 @@ int mnb_rope_append(const void *q, int64_t q_ts, int64_t q_hs, const void *k, in
             return fail(MNB_ERR_ALIGN, "%s: a pointer is not 16-byte aligned", fn);
     if (!aligned(slots, 4) || !aligned(positions, 4) || !aligned(status, 4))
         return fail(MNB_ERR_ALIGN, "%s: slots, positions and status need 4-byte alignment", fn);
+    if (T == 1)
+        q_ts = k_ts = v_ts = o_ts = 0;
+    if (Hq <= 1)
+        q_hs = o_hs = 0;
+    if (Hq == 0)
+        q_ts = o_ts = 0;
+    if (cache->num_heads == 1)
+        k_hs = v_hs = 0;
     for (int64_t st : {q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs})
         if ((rc = check_stride(fn, st, cache->dtype)))
             return rc;
@@ -593,13 +612,14 @@ size_t mnb_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, i
     return paged_attention_workspace_bytes((int)Hq, (int)Hkv, (int)D, dtype == MNB_F16);
 }
 
-int mnb_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_paged_cache *cache,
+int mnb_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_paged_cache *given,
                         const int32_t *block_table, int64_t table_stride, int64_t max_blocks, const int32_t *seq_lens,
                         int64_t B, int64_t Hq, float scale, void *out, int64_t o_bs, int64_t o_hs, float *lse,
                         void *workspace, size_t ws_bytes, int *status, unsigned flags, void *stream) {
     clear_error();
     const char *fn = "mnb_paged_attention";
-    int rc = check_paged_cache(fn, cache);
+    mnb_paged_cache pool, *cache = &pool;
+    int rc = check_paged_cache(fn, given, cache);
     if (rc)
         return rc;
     if (B < 0 || Hq < 1)
@@ -625,6 +645,10 @@ int mnb_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_pag
         return fail(MNB_ERR_ALIGN, "%s: q, out and workspace must be 16-byte aligned", fn);
     if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(status, 4))
         return fail(MNB_ERR_ALIGN, "%s: block_table, seq_lens, lse and status need 4-byte alignment", fn);
+    if (B == 1)
+        q_bs = o_bs = 0;
+    if (Hq == 1)
+        q_hs = o_hs = 0;
     for (int64_t st : {q_bs, q_hs, o_bs, o_hs})
         if ((rc = check_stride(fn, st, cache->dtype)))
             return rc;

@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCtas = 3;   // per SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -55,16 +56,18 @@ struct AttnParams {
     float scale;
 };
 
-// Element type, padded head size, rows of query heads per segment.
+// Element type, padded head size, rows of query heads per segment.  A tile is
+// 8 KB of K and V (16 KB for heads of 256): 16 keys of 128 fp16 entries.
 template <typename T_, int DP_, int ROWS_, int STAGES_>
 struct Cfg {
     using T = T_;
     static constexpr bool F16 = std::is_same<T, half>::value;
     static constexpr int DP = DP_, ROWS = ROWS_, STAGES = STAGES_;
-    static constexpr int TK = F16 ? 16 : 8;                 // keys per tile
-    static constexpr int NCH = DP * (int)sizeof(T) / 16;    // 16-byte chunks per row
+    static constexpr int TK = (F16 ? 16 : 8) * (DP <= 64 ? 2 : 1);   // keys per tile
+    static constexpr int NCH = DP * (int)sizeof(T) / 16;             // 16-byte chunks per row
     static constexpr int ROW_BYTES = DP * (int)sizeof(T);
     static constexpr int TILE_BYTES = TK * ROW_BYTES;
+    static constexpr int kCtas = DP > 128 ? 1 : kMaxCtas;                          // CTAs on an SM, as far as registers go
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
@@ -148,141 +151,221 @@ __device__ __forceinline__ void advance(const Shared &sh, Cursor &c) {
     } while (c.tiles == 0);
 }
 
-// The running softmax of one segment in a warp's registers.
+// Two neighbouring outputs of one row; c is even and below D (a multiple of 8).
+__device__ __forceinline__ void store2(half *p, float a, float b) { *reinterpret_cast<half2 *>(p) = __floats2half2_rn(a, b); }
+__device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
+
+// The transpose of an 8x8 matrix of 16-bit values, one packed pair per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// log sum exp from a maximum in log2 units and a sum relative to it.
+__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? m * kLn2 + logf(l) : -INFINITY; }
+
+// The running softmax of one segment in a warp's registers.  The maximum m is a
+// reference, not the exact maximum: it moves, and o and l are rescaled, only
+// when a score exceeds it by more than 2^LAZY (in most tiles one vote says that
+// none does, and no maximum is taken across lanes).
+constexpr float LAZY = 5.0f;
+
 template <typename C, bool F16>
 struct Acc;
 
-// fp16: S = Q K^T and O += P V as m16n8k16 products with the query heads as the
-// 16 rows (rows at and above ROWS are zero).  P is rounded to fp16 with its
-// row's maximum at 2^10, so that terms down to 2^-24 of the largest keep their
-// 11 bits; l is summed from the unrounded fp32 values.
+// fp16: S^T = K Q^T and O^T += V^T P^T as m16n8k16 products: keys, then head
+// entries are the 16 rows, up to 8 query heads the 8 columns (the grouped heads
+// of one KV head seldom fill more).  P is rounded to fp16 for the second
+// product, scaled so that the reference maximum is at 2^SHIFT: its largest
+// values stay below 2^15, and terms down to 2^-24 of the largest keep their 11
+// bits.  l is summed from the unrounded fp32 values.
 template <typename C>
 struct Acc<C, true> {
-    static constexpr int HALVES = C::ROWS > 8 ? 2 : 1;
+    static constexpr int NT = C::ROWS / 8, KB = C::TK / 16, KS = C::DP / 16;
     static constexpr float SHIFT = 10.0f;
-    float o[C::DP / 8][4];
-    float m[2], l[2];
-    uint32_t q[C::DP / 16][2 * HALVES];   // A fragments of the segment's query rows
+    static constexpr float kSumScale = 1.0f / 1024.0f;   // 2^-SHIFT
+    float o[KS][NT][4];        // entry 16 i + lane / 4 (+ 8), heads 2 (lane % 4) and the next
+    float m[NT][2], l[NT][2];
+    uint32_t q[KS][NT][2];     // B fragments of the segment's query rows
 
     // The segment's query rows, just landed at `qs`.
     __device__ __forceinline__ void open(uint32_t qs, uint32_t, int rows) {
-        const int lane = threadIdx.x & 31;
-        const int qr = min((lane & 7) + (HALVES == 2 ? ((lane >> 3) & 1) * 8 : 0), rows - 1), qc = lane >> 4;
+        const int lane = threadIdx.x & 31, i = lane >> 3;
+        if constexpr (NT == 1) {
+            const int r = min(lane & 7, rows - 1);
 #pragma unroll
-        for (int kk = 0; kk < C::DP / 16; kk++) {
-            uint32_t a0, a1, a2, a3;
-            ldsm4(qs + qr * C::ROW_BYTES + (((kk * 2 + qc) ^ (qr & 7)) << 4), a0, a1, a2, a3);
-            q[kk][0] = a0, q[kk][1] = a2;
-            if (HALVES == 2)
-                q[kk][HALVES] = a1, q[kk][HALVES + 1] = a3;
+            for (int kk = 0; kk < KS; kk += 2)
+                ldsm4(qs + r * C::ROW_BYTES + (((kk * 2 + i) ^ (r & 7)) << 4), q[kk][0][0], q[kk][0][1], q[kk + 1][0][0],
+                      q[kk + 1][0][1]);
+        } else {
+            const int r = min((lane & 7) + (i >> 1) * 8, rows - 1);
+#pragma unroll
+            for (int kk = 0; kk < KS; kk++)
+                ldsm4(qs + r * C::ROW_BYTES + (((kk * 2 + (i & 1)) ^ (r & 7)) << 4), q[kk][0][0], q[kk][0][1],
+                      q[kk][NT - 1][0], q[kk][NT - 1][1]);
         }
-        reset();
-    }
-
-    __device__ __forceinline__ void reset() {
 #pragma unroll
-        for (int n = 0; n < C::DP / 8; n++)
-            o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.0f;
+        for (int t = 0; t < NT; t++) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KS; k++)
+                o[k][t][0] = o[k][t][1] = o[k][t][2] = o[k][t][3] = 0.0f;
+        }
     }
 
     // One tile: K and V in shared memory, `valid` one bit per key.
     __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t, int, uint32_t valid, float scale2) {
-        const int lane = threadIdx.x & 31, t2 = (lane & 3) * 2;
-        float s[2][4] = {};
-        const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+        const int lane = threadIdx.x & 31, g = lane >> 2;
+        float s[KB][NT][4];
+        {
+            float h[2][KB][NT][4] = {};   // even and odd steps: two chains of products
+            const int kr = (lane & 7) + ((lane >> 3) & 1) * 8, kc = lane >> 4;
 #pragma unroll
-        for (int kk = 0; kk < C::DP / 16; kk++) {
-            uint32_t b0, b1, b2, b3;
-            const uint32_t a0 = q[kk][0], a2 = q[kk][1];
-            const uint32_t a1 = HALVES == 2 ? q[kk][HALVES] : 0u, a3 = HALVES == 2 ? q[kk][2 * HALVES - 1] : 0u;
-            ldsm4(ks + kr * C::ROW_BYTES + (((kk * 2 + kc) ^ (kr & 7)) << 4), b0, b1, b2, b3);
-            mma16816(s[0], a0, a1, a2, a3, b0, b1);
-            mma16816(s[1], a0, a1, a2, a3, b2, b3);
+            for (int kk = 0; kk < KS; kk++)
+#pragma unroll
+                for (int b = 0; b < KB; b++) {
+                    uint32_t a0, a1, a2, a3;
+                    ldsm4(ks + (b * 16 + kr) * C::ROW_BYTES + (((kk * 2 + kc) ^ (kr & 7)) << 4), a0, a1, a2, a3);
+#pragma unroll
+                    for (int t = 0; t < NT; t++)
+                        mma16816(h[kk & 1][b][t], a0, a1, a2, a3, q[kk][t][0], q[kk][t][1]);
+                }
+#pragma unroll
+            for (int b = 0; b < KB; b++)
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+                        s[b][t][c] = h[0][b][t][c] + h[1][b][t][c];
         }
-        float mn[2] = {m[0], m[1]};
+        bool over = false;
 #pragma unroll
-        for (int n = 0; n < 2; n++)
+        for (int b = 0; b < KB; b++)
 #pragma unroll
             for (int c = 0; c < 4; c++) {
-                const bool ok = (valid >> (n * 8 + t2 + (c & 1))) & 1;
-                s[n][c] = ok ? s[n][c] * scale2 : -INFINITY;
-                mn[c >> 1] = fmaxf(mn[c >> 1], s[n][c]);
+                const bool ok = (valid >> (b * 16 + g + (c >> 1) * 8)) & 1;
+#pragma unroll
+                for (int t = 0; t < NT; t++) {
+                    s[b][t][c] = ok ? s[b][t][c] * scale2 : -INFINITY;
+                    over |= s[b][t][c] > m[t][c & 1] + LAZY;
+                }
             }
-        uint32_t p[2][2];   // [key half][row half], packed pairs
-        bool grew = false;
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-        for (int h = 0; h < HALVES; h++) {
-            mn[h] = fmaxf(mn[h], __shfl_xor_sync(0xffffffffu, mn[h], 1));
-            mn[h] = fmaxf(mn[h], __shfl_xor_sync(0xffffffffu, mn[h], 2));
-            grew |= mn[h] > m[h];
+            for (int t = 0; t < NT; t++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    float mn = m[t][c];
+#pragma unroll
+                    for (int b = 0; b < KB; b++)
+                        mn = fmaxf(mn, fmaxf(s[b][t][c], s[b][t][c + 2]));
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1)
+                        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+                    const float alpha = mn > m[t][c] ? ex2(m[t][c] - mn) : 1.0f;   // 0 after m = -inf
+                    m[t][c] = mn;
+                    l[t][c] *= alpha;
+#pragma unroll
+                    for (int k = 0; k < KS; k++)
+                        o[k][t][c] *= alpha, o[k][t][c + 2] *= alpha;
+                }
         }
-        if (__any_sync(0xffffffffu, grew)) {
+        uint32_t p[KB][NT][2];
 #pragma unroll
-            for (int h = 0; h < HALVES; h++) {
-                const float alpha = mn[h] > m[h] ? ex2(m[h] - mn[h]) : 1.0f;   // 0 after m = -inf
-                m[h] = mn[h];
-                l[h] *= alpha;
+        for (int t = 0; t < NT; t++) {
+            const float b0 = m[t][0] == -INFINITY ? 0.0f : m[t][0] - SHIFT;
+            const float b1 = m[t][1] == -INFINITY ? 0.0f : m[t][1] - SHIFT;
 #pragma unroll
-                for (int n = 0; n < C::DP / 8; n++)
-                    o[n][2 * h] *= alpha, o[n][2 * h + 1] *= alpha;
+            for (int b = 0; b < KB; b++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const float x = ex2(s[b][t][2 * h] - b0), y = ex2(s[b][t][2 * h + 1] - b1);
+                    l[t][0] += x, l[t][1] += y;
+                    p[b][t][h] = transpose8(h2_as_u32(__floats2half2_rn(x, y)));
+                }
+        }
+        const int vr = (lane & 7) + (lane >> 4) * 8, vc = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < KS; k++)
+#pragma unroll
+            for (int b = 0; b < KB; b++) {
+                uint32_t a0, a1, a2, a3;
+                ldsm4t(vs + (b * 16 + vr) * C::ROW_BYTES + (((k * 2 + vc) ^ (vr & 7)) << 4), a0, a1, a2, a3);
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+                    mma16816(o[k][t], a0, a1, a2, a3, p[b][t][0], p[b][t][1]);
             }
-        }
-#pragma unroll
-        for (int h = 0; h < HALVES; h++) {
-            const float base = m[h] == -INFINITY ? 0.0f : m[h] - SHIFT;
-#pragma unroll
-            for (int n = 0; n < 2; n++) {
-                const float x = ex2(s[n][2 * h] - base), y = ex2(s[n][2 * h + 1] - base);
-                l[h] += x + y;
-                p[n][h] = h2_as_u32(__floats2half2_rn(x, y));
-            }
-        }
-        if (HALVES == 1)
-            p[0][1] = p[1][1] = 0;
-        const int vr = lane & 15, vc = lane >> 4;
-#pragma unroll
-        for (int n = 0; n < C::DP / 16; n++) {
-            uint32_t b0, b1, b2, b3;
-            ldsm4t(vs + vr * C::ROW_BYTES + (((n * 2 + vc) ^ (vr & 7)) << 4), b0, b1, b2, b3);
-            mma16816(o[2 * n], p[0][0], p[0][1], p[1][0], p[1][1], b0, b1);
-            mma16816(o[2 * n + 1], p[0][0], p[0][1], p[1][0], p[1][1], b2, b3);
-        }
     }
 
+    // Sums over the lanes' keys.
     __device__ __forceinline__ void finish() {
 #pragma unroll
-        for (int h = 0; h < HALVES; h++) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        }
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+            for (int c = 0; c < 2; c++)
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1)
+                    l[t][c] += __shfl_xor_sync(0xffffffffu, l[t][c], x);
     }
 
-    // f(row, column, value, value) over pairs of columns; g(row, m, l) once per row.
-    template <typename F, typename H>
-    __device__ __forceinline__ void each(F f, H g) {
-        const int lane = threadIdx.x & 31, r0 = lane >> 2, t2 = (lane & 3) * 2;
+    // A partial result: rows x D outputs, maxima, sums.
+    __device__ __forceinline__ void to_slot(float *sl, int rows, int D) {
+        const int lane = threadIdx.x & 31, g = lane >> 2;
 #pragma unroll
-        for (int h = 0; h < HALVES; h++) {
+        for (int t = 0; t < NT; t++)
 #pragma unroll
-            for (int n = 0; n < C::DP / 8; n++)
-                f(r0 + 8 * h, n * 8 + t2, o[n][2 * h], o[n][2 * h + 1], m[h], l[h]);
-            if (t2 == 0)
-                g(r0 + 8 * h, m[h], l[h]);
+            for (int c = 0; c < 2; c++) {
+                const int r = t * 8 + (lane & 3) * 2 + c;
+                if (r < rows) {
+#pragma unroll
+                    for (int k = 0; k < 2 * KS; k++)
+                        if (k * 8 < D)
+                            sl[r * D + k * 8 + g] = o[k / 2][t][c + 2 * (k & 1)];
+                    if (g == 0) {
+                        sl[rows * D + r] = m[t][c];
+                        sl[rows * D + rows + r] = l[t][c];
+                    }
+                }
+            }
+    }
+
+    // The finished rows: row(r) is the query head of row r, or -1.
+    template <typename F>
+    __device__ __forceinline__ void to_out(half *out, int64_t hs, float *lse, int D, F row) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t2 = (lane & 3) * 2;
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+            const float i0 = l[t][0] > 0.0f ? 1.0f / l[t][0] : 0.0f, i1 = l[t][1] > 0.0f ? 1.0f / l[t][1] : 0.0f;
+            const int head = row(t * 8 + g);
+            half *p = out + head * hs + t2;
+#pragma unroll
+            for (int k = 0; k < 2 * KS; k++) {
+                const int h = 2 * (k & 1);
+                const uint32_t v = transpose8(h2_as_u32(__floats2half2_rn(o[k / 2][t][h] * i0, o[k / 2][t][h + 1] * i1)));
+                if (head >= 0 && k * 8 < D)
+                    *reinterpret_cast<uint32_t *>(p + k * 8) = v;
+            }
+            if (lse && g < 2) {
+                const int hl = row(t * 8 + t2 + g);
+                if (hl >= 0)
+                    lse[hl] = lse_of(g ? m[t][1] : m[t][0], (g ? l[t][1] : l[t][0]) * kSumScale);
+            }
         }
     }
-    static constexpr float kSumScale = 1.0f / 1024.0f;   // 2^-SHIFT
 };
 
-// fp32: every product and sum in fp32 on the CUDA cores.  Scores: a lane holds
-// key lane % 8 and a quarter of the chunks, two shuffles add the quarters.
-// Output: a lane holds whole columns; a row's probabilities come by shuffle.
+// fp32: every product and sum in fp32 on the CUDA cores, eight keys at a time.
+// Scores: a lane holds key lane % 8 and a quarter of the chunks, two shuffles
+// add the quarters.  Output: a lane holds whole columns; a row's probabilities
+// come by shuffle.
 template <typename C>
 struct Acc<C, false> {
     static constexpr int LPR = C::NCH < 32 ? C::NCH : 32;   // lanes per row of V
     static constexpr int PER = C::NCH / LPR;                // chunks a lane holds
     static constexpr int KSPLIT = 32 / LPR;                 // keys taken at a time
+    static constexpr float kSumScale = 1.0f;
     float4 o[C::ROWS][PER];
     float m[C::ROWS], l[C::ROWS];
 
@@ -295,10 +378,6 @@ struct Acc<C, false> {
                          : "memory");
         }
         __syncwarp();
-        reset();
-    }
-
-    __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int r = 0; r < C::ROWS; r++) {
 #pragma unroll
@@ -310,6 +389,12 @@ struct Acc<C, false> {
     }
 
     __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t qs, int rows, uint32_t valid, float scale2) {
+#pragma unroll
+        for (int j = 0; j < C::TK / 8; j++)
+            eight(ks + j * 8 * C::ROW_BYTES, vs + j * 8 * C::ROW_BYTES, qs, rows, valid >> (8 * j), scale2);
+    }
+
+    __device__ __forceinline__ void eight(uint32_t ks, uint32_t vs, uint32_t qs, int rows, uint32_t valid, float scale2) {
         const int lane = threadIdx.x & 31, key = lane & 7, quarter = lane >> 3;
         float s[C::ROWS] = {};
 #pragma unroll 4
@@ -323,24 +408,32 @@ struct Acc<C, false> {
             }
         }
         const bool ok = (valid >> key) & 1;
+        bool over = false;
 #pragma unroll
         for (int r = 0; r < C::ROWS; r++) {
             s[r] += __shfl_xor_sync(0xffffffffu, s[r], 8);
             s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
             s[r] = ok ? s[r] * scale2 : -INFINITY;
-            float mn = fmaxf(m[r], s[r]);
+            over |= s[r] > m[r] + LAZY;
+        }
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-            for (int x = 1; x < 8; x <<= 1)
-                mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
-            if (mn > m[r]) {   // the same in every lane
-                const float alpha = ex2(m[r] - mn);
+            for (int r = 0; r < C::ROWS; r++) {
+                float mn = fmaxf(m[r], s[r]);
+#pragma unroll
+                for (int x = 1; x < 8; x <<= 1)
+                    mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+                const float alpha = mn > m[r] ? ex2(m[r] - mn) : 1.0f;
                 m[r] = mn;
                 l[r] *= alpha;
 #pragma unroll
                 for (int c = 0; c < PER; c++)
                     o[r][c].x *= alpha, o[r][c].y *= alpha, o[r][c].z *= alpha, o[r][c].w *= alpha;
             }
-            s[r] = mn == -INFINITY ? 0.0f : ex2(s[r] - mn);
+        }
+#pragma unroll
+        for (int r = 0; r < C::ROWS; r++) {
+            s[r] = m[r] == -INFINITY ? 0.0f : ex2(s[r] - m[r]);
             l[r] += s[r];   // this lane's key; the eight keys are added in finish()
         }
         const int col = lane % LPR, sub = lane / LPR;
@@ -379,32 +472,42 @@ struct Acc<C, false> {
         }
     }
 
-    template <typename F, typename H>
-    __device__ __forceinline__ void each(F f, H g) {
+    __device__ __forceinline__ void to_slot(float *sl, int rows, int D) {
         const int lane = threadIdx.x & 31, col = lane % LPR;
-        if (lane >= LPR)
-            return;
 #pragma unroll
         for (int r = 0; r < C::ROWS; r++) {
+            if (r >= rows)
+                break;
 #pragma unroll
-            for (int c = 0; c < PER; c++) {
-                const int e = (col + c * 32) * 4;
-                f(r, e, o[r][c].x, o[r][c].y, m[r], l[r]);
-                f(r, e + 2, o[r][c].z, o[r][c].w, m[r], l[r]);
+            for (int c = 0; c < PER; c++)
+                if (lane < LPR && (col + c * 32) * 4 < D)
+                    *reinterpret_cast<float4 *>(sl + r * D + (col + c * 32) * 4) = o[r][c];
+            if (lane == 0) {
+                sl[rows * D + r] = m[r];
+                sl[rows * D + rows + r] = l[r];
             }
-            if (lane == 0)
-                g(r, m[r], l[r]);
         }
     }
-    static constexpr float kSumScale = 1.0f;
+
+    template <typename F>
+    __device__ __forceinline__ void to_out(float *out, int64_t hs, float *lse, int D, F row) {
+        const int lane = threadIdx.x & 31, col = lane % LPR;
+#pragma unroll
+        for (int r = 0; r < C::ROWS; r++) {
+            const int head = row(r);
+            if (head < 0)
+                continue;
+            const float inv = l[r] > 0.0f ? 1.0f / l[r] : 0.0f;
+#pragma unroll
+            for (int c = 0; c < PER; c++)
+                if (lane < LPR && (col + c * 32) * 4 < D)
+                    *reinterpret_cast<float4 *>(out + head * hs + (col + c * 32) * 4) =
+                        make_float4(o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv);
+            if (lane == 0 && lse)
+                lse[head] = lse_of(m[r], l[r]);
+        }
+    }
 };
-
-// Two neighbouring outputs of one row; c is even and below D (a multiple of 8).
-__device__ __forceinline__ void store2(half *p, float a, float b) { *reinterpret_cast<half2 *>(p) = __floats2half2_rn(a, b); }
-__device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
-
-// log sum exp from a maximum in log2 units and a sum relative to it.
-__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? m * kLn2 + logf(l) : -INFINITY; }
 
 // A partial result in memory: rows x D outputs, then rows maxima, then rows sums
 // (relative to the maximum, as o is), to a multiple of 16 bytes.
@@ -429,7 +532,7 @@ struct Chain {
 };
 
 template <typename C>
-__global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_kernel(const __grid_constant__ AttnParams p) {
     using T = typename C::T;
     using A = Acc<C, C::F16>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -453,11 +556,12 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
     pdl_wait();
     pdl_launch_dependents();
 
-    // tiles of each request, and their sums
+    // tiles of each request, and their sums; up to 32 requests: by every warp for itself, to the same words
     uint32_t carry = 0;
     bool bad_len = false;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-        const int b = b0 + (int)threadIdx.x;
+    const bool alone = p.B <= 32;
+    for (int b0 = 0; b0 < p.B; b0 += alone ? 32 : kThreads) {
+        const int b = b0 + (alone ? lane : (int)threadIdx.x);
         uint32_t v = 0;
         if (b < p.B) {
             const int n = p.lens[b];
@@ -470,20 +574,24 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
             if (lane >= o)
                 v += u;
         }
-        __syncthreads();
-        if (lane == 31)
-            warp_sums[warp] = v;
-        __syncthreads();
-        uint32_t before = carry;
+        if (alone) {
+            carry = __shfl_sync(0xffffffffu, v, 31);
+        } else {
+            __syncthreads();
+            if (lane == 31)
+                warp_sums[warp] = v;
+            __syncthreads();
+            v += carry;
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            before += w < warp ? warp_sums[w] : 0u;
-            carry += warp_sums[w];
+            for (int w = 0; w < kWarps; w++) {
+                v += w < warp ? warp_sums[w] : 0u;
+                carry += warp_sums[w];
+            }
         }
         if (b < p.B)
-            prefix[b + 1] = v + before;
+            prefix[b + 1] = v;
     }
-    if (threadIdx.x == 0)
+    if (lane == 0)
         prefix[0] = 0;
     if (threadIdx.x <= kWarps)
         chains[threadIdx.x].parts = 0;
@@ -519,7 +627,7 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
     // the query head of row r of a segment, or -1 past the group
     auto head_of = [&](int seg, int r) -> int {
         if (p.row_tiles == 1)
-            return r < p.G ? seg * p.G + r : -1;
+            return r < p.G ? seg * p.G + r : -1;   // G = rows
         const int h = seg / p.row_tiles, i = (seg - h * p.row_tiles) * C::ROWS + r;
         return r < p.rows && i < p.G ? h * p.G + i : -1;
     };
@@ -536,8 +644,11 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
         int64_t head_off = (p.row_tiles == 1 ? load.seg : load.seg / p.row_tiles) * p.head_stride;
         // the next tile's table entries, on the way while earlier tiles are issued: lane i holds key i
         int ent = -1, ent_off = 0;
+        uint32_t want = 0;   // its keys, a bit each
         auto fetch = [&]() {
             const int key = (int)load.tile * C::TK + lane;
+            const int n = len - (int)load.tile * C::TK;
+            want = n < C::TK ? (1u << n) - 1 : C::TK == 32 ? 0xffffffffu : (1u << C::TK % 32) - 1;
             ent = -1;
             if (lane < C::TK && key < len) {
                 const int blk = p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
@@ -561,9 +672,9 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
                 return 0;
             }
             const bool has = ent >= 0 && ent < p.num_pages;
-            if (!has && lane < C::TK && (int)load.tile * C::TK + lane < len && p.status)
-                atomicOr(p.status, 1);
             const uint32_t valid = __ballot_sync(0xffffffffu, has);
+            if (valid != want && p.status)
+                atomicOr(p.status, 1);
             const int64_t off = has ? ent * p.page_stride + ent_off * p.slot_stride + head_off : 0;
             constexpr int RPI = C::NCH >= 32 ? 1 : 32 / C::NCH;      // rows per instruction
             constexpr int CPL = C::NCH > 32 ? C::NCH / 32 : 1;       // chunks of a row per lane
@@ -606,11 +717,12 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
         bool opened = cur.tile == 0;   // the segment's first tile is this warp's
         int stage = 0;
         while (todo > 0) {
-            cp_wait<C::STAGES - 2>();
-            __syncwarp();
-            const int ahead = stage == 0 ? C::STAGES - 1 : stage - 1;   // the stage that the last item left
+            __syncwarp();   // every lane has read the stage that the last item left: it takes the next one
+            const int ahead = stage == 0 ? C::STAGES - 1 : stage - 1;
             const uint32_t nv = left > 0 ? issue(ahead) : 0u;
             cp_commit();
+            cp_wait<C::STAGES - 1>();
+            __syncwarp();
             const uint32_t ks = smem_u32(ring) + stage * 2 * C::TILE_BYTES;
             const uint32_t valid = vmask[0];
 #pragma unroll
@@ -629,34 +741,11 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
             if (ends || todo == 0) {
                 acc.finish();
                 if (opened && ends) {
-                    T *o = (T *)p.out + cur.b * p.o_bs;
-                    acc.each(
-                        [&](int r, int c, float x, float y, float, float l) {
-                            const int head = head_of(cur.seg, r);
-                            if (head >= 0 && c < p.D) {
-                                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                                store2(o + head * p.o_hs + c, x * inv, y * inv);
-                            }
-                        },
-                        [&](int r, float m, float l) {
-                            const int head = head_of(cur.seg, r);
-                            if (head >= 0 && p.lse)
-                                p.lse[(int64_t)cur.b * Hq + head] = lse_of(m, l * A::kSumScale);
-                        });
+                    acc.to_out((T *)p.out + cur.b * p.o_bs, p.o_hs, p.lse ? p.lse + (int64_t)cur.b * Hq : nullptr, p.D,
+                               [&](int r) { return head_of(cur.seg, r); });
                 } else {
                     __syncwarp();   // every lane has read the last tile of a ring that is written over
-                    float *sl = slot_of(warp, opened);
-                    acc.each(
-                        [&](int r, int c, float x, float y, float, float) {
-                            if (r < p.rows && c < p.D)
-                                *reinterpret_cast<float2 *>(sl + r * p.D + c) = make_float2(x, y);
-                        },
-                        [&](int r, float m, float l) {
-                            if (r < p.rows) {
-                                sl[p.rows * p.D + r] = m;
-                                sl[p.rows * p.D + p.rows + r] = l;
-                            }
-                        });
+                    acc.to_slot(slot_of(warp, opened), p.rows, p.D);
                     if (opened && lane == 0) {   // and todo == 0: the segment goes on in the next warp
                         const uint32_t first = w1 - 1 - cur.tile, end = first + cur.tiles;
                         chains[1 + warp] = {warp, (int)range_of(c1 - c0, kWarps, min(end, c1) - 1 - c0) - warp + 1,
@@ -819,20 +908,21 @@ __global__ void __launch_bounds__(kThreads) paged_attention_kernel(const __grid_
 }
 
 constexpr size_t kSmemMax = 227 * 1024 - 256;
-constexpr size_t kSmemTwo = 113 * 1024 - 256;   // two CTAs on an SM
+constexpr size_t kSmemSm = 228 * 1024;
 
 template <typename C>
 int launch_cfg(const AttnParams &p, int most, size_t smem, unsigned flags, cudaStream_t s) {
-    const int resident = device_sm_count() * (smem <= kSmemTwo ? 2 : 1);
-    // the last join keeps two floats per row and part, and 16 bytes per thread, in the rings
-    const int joinable = (kWarps * C::STAGES * 2 * C::TILE_BYTES - kThreads * 16 - 16) / (8 * p.rows);
-    int grid = most < resident ? most : resident;
-    grid = grid < joinable ? grid : joinable;
     static int cache[kMaxDevices] = {};
     auto *kernel = paged_attention_kernel<C>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)smem, cache);
     if (e != cudaSuccess)
         return fail(MNB_ERR_CUDA, "mnb_paged_attention: %s", cudaGetErrorString(e));
+    const int by_smem = (int)(kSmemSm / (smem + 1024 + 256));
+    const int resident = device_sm_count() * (by_smem < C::kCtas ? by_smem : C::kCtas);
+    // the last join keeps two floats per row and part, and 16 bytes per thread, in the rings
+    const int joinable = (kWarps * C::STAGES * 2 * C::TILE_BYTES - kThreads * 16 - 16) / (8 * p.rows);
+    int grid = most < resident ? most : resident;
+    grid = grid < joinable ? grid : joinable;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
@@ -860,14 +950,11 @@ size_t smem_bytes(int rows, int D, int B) {
 
 template <typename T, int DP, int ROWS>
 int launch_rows(const AttnParams &p, int most, unsigned flags, cudaStream_t s) {
-    using C2 = Cfg<T, DP, ROWS, 2>;
-    using C3 = Cfg<T, DP, ROWS, 3>;
-    const size_t s2 = smem_bytes<C2>(p.rows, p.D, p.B), s3 = smem_bytes<C3>(p.rows, p.D, p.B);
-    if (s3 <= kSmemTwo)
-        return launch_cfg<C3>(p, most, s3, flags, s);
-    if (s2 > kSmemMax)
-        return fail(MNB_ERR_UNSUPPORTED, "mnb_paged_attention: %zu bytes of shared memory needed", s2);
-    return launch_cfg<C2>(p, most, s2, flags, s);
+    using C = Cfg<T, DP, ROWS, 2>;
+    const size_t smem = smem_bytes<C>(p.rows, p.D, p.B);
+    if (smem > kSmemMax)
+        return fail(MNB_ERR_UNSUPPORTED, "mnb_paged_attention: %zu bytes of shared memory needed", smem);
+    return launch_cfg<C>(p, most, smem, flags, s);
 }
 
 template <typename T, int DP>
@@ -882,7 +969,7 @@ int launch_dp(const AttnParams &p, int ctas, unsigned flags, cudaStream_t s) {
 }
 
 int rows_per_segment(int G, int f16) { return G < (f16 ? 16 : 8) ? G : (f16 ? 16 : 8); }
-int grid_of() { return device_sm_count() * 2; }
+int grid_of() { return device_sm_count() * kMaxCtas; }
 size_t counters_bytes() { return ((size_t)grid_of() * 4 + 127) / 128 * 128; }
 
 }  // namespace

@@ -133,12 +133,24 @@ def test_binding_refuses_tensors(mnb):
     with pytest.raises(mnb.MnbError, match="current CUDA device"):
         mnb.mnb_paged_attention(q, kv, kv, tab, i, 0.1, q, ws)
     with pytest.raises(mnb.MnbError, match="current CUDA device"):
-        mnb.mnb_paged_tables(i, i, tab, 16, 3, i, i[:1], i, i, i, i, i[:1])
+        mnb.mnb_paged_tables(i, i, tab, 16, 3, i, i[:1], i, torch.zeros(5, dtype=torch.int32), i, i, i[:1])
     with pytest.raises(mnb.MnbError, match="current CUDA device"):
-        mnb.mnb_rope_append(q, q, q, kv, kv, i, None, None, None, q)
+        mnb.mnb_rope_append(q, q[:, :2], q[:, 2:], kv, kv, i, None, None, None, q)
     with pytest.raises(mnb.MnbError, match="fp16 or fp32"):
         mnb.mnb_paged_attention(q, kv.bfloat16(), kv.bfloat16(), tab, i, 0.1, q, ws)
-    with pytest.raises(mnb.MnbError, match="one shape"):
+    with pytest.raises(mnb.MnbError, match="v_cache has shape"):
         mnb.mnb_paged_attention(q, kv, kv[:2], tab, i, 0.1, q, ws)
+    with pytest.raises(mnb.MnbError, match="v_cache is torch.float32"):
+        mnb.mnb_paged_attention(q, kv, kv.float(), tab, i, 0.1, q, ws)
+    with pytest.raises(mnb.MnbError, match="q has shape"):
+        mnb.mnb_paged_attention(q[0], kv, kv, tab, i, 0.1, q, ws)
+    with pytest.raises(mnb.MnbError, match="k_cache's strides"):
+        mnb.mnb_paged_attention(q, kv, kv.transpose(1, 2).contiguous().transpose(1, 2), tab, i, 0.1, q, ws)
+    with pytest.raises(mnb.MnbError, match="k has shape"):
+        mnb.mnb_rope_append(None, q, kv[0, :4], kv, kv, i, None, None, None, None)
+    with pytest.raises(mnb.MnbError, match="v_cache's last dimension"):
+        mnb.mnb_paged_attention(q, kv, kv.transpose(1, 3).contiguous().transpose(1, 3), tab, i, 0.1, q, ws)
+    with pytest.raises(mnb.MnbError, match="cu_new has shape"):
+        mnb.mnb_paged_tables(i, i, tab, 16, 3, i, i[:1], i, i, i, i, i[:1])
     with pytest.raises(mnb.MnbError, match="go together"):
         mnb.mnb_rope_append(None, q, q, kv, kv, i, None, None, None, q)
