@@ -33,6 +33,11 @@ MNB_API int mnb_tune_gemv_split(int w, int s);
  * it; 0 runs the general decode kernel. */
 MNB_API int mnb_tune_gemv_resident(int enable);
 
+/* mnb_paged_attention: which kernel runs -- 0 (default) by the call's sizes,
+ * 1 the one that cuts the list of all tiles into equal ranges, 2 the one that
+ * joins a segment's parts inside a cluster. */
+MNB_API int mnb_tune_paged_attention(int mode);
+
 /* Fault injection for tests of mnb_gemv_chain's timeout path (no GPU fault,
  * no hang): every later launch leaves task `task` uncounted, so the next task
  * that waits for it gives up after wait_limit_us microseconds (0 = the

@@ -28,6 +28,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "mnb_tune.h"
 
 namespace mnb {
 namespace {
@@ -35,6 +36,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 3;   // per SM
+constexpr int kClusterTiles = 16;   // most tiles a warp of the cluster kernel may have
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -51,8 +53,10 @@ struct AttnParams {
     int64_t table_stride, page_stride, slot_stride, head_stride;
     int B, G, Hkv, D, rows, row_tiles, page, num_pages, cap;   // cap: rows the table has room for
     int page_shift;                                        // log2(page), -1 if it is no power of two
+    int one_page;                                          // a tile's keys are in one page: page % TK == 0
     int min_tiles;                                         // fewest tiles worth a CTA
     float join_cost;                                       // of a partial result in the last join, in tiles
+    int split_shift;                                       // cluster kernel: log2 of the CTAs per segment
     float scale;
 };
 
@@ -67,7 +71,7 @@ struct Cfg {
     static constexpr int NCH = DP * (int)sizeof(T) / 16;             // 16-byte chunks per row
     static constexpr int ROW_BYTES = DP * (int)sizeof(T);
     static constexpr int TILE_BYTES = TK * ROW_BYTES;
-    static constexpr int kCtas = DP > 128 ? 1 : kMaxCtas;                          // CTAs on an SM, as far as registers go
+    static constexpr int kCtas = DP > 128 ? 1 : !F16 && ROWS > 4 ? 2 : kMaxCtas;                          // CTAs on an SM, as far as registers go
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
@@ -389,7 +393,7 @@ struct Acc<C, false> {
     }
 
     __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t qs, int rows, uint32_t valid, float scale2) {
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < C::TK / 8; j++)
             eight(ks + j * 8 * C::ROW_BYTES, vs + j * 8 * C::ROW_BYTES, qs, rows, valid >> (8 * j), scale2);
     }
@@ -509,6 +513,81 @@ struct Acc<C, false> {
     }
 };
 
+// A warp's copies into its ring: lane i holds the table entry of key i of the
+// next tile, loaded while earlier tiles are under way.
+template <typename C>
+struct Feed {
+    using T = typename C::T;
+    static constexpr int EPC = 16 / (int)sizeof(T);                 // entries per chunk
+    static constexpr int RPI = C::NCH >= 32 ? 1 : 32 / C::NCH;      // rows per instruction
+    static constexpr int CPL = C::NCH > 32 ? C::NCH / 32 : 1;       // chunks of a row per lane
+    const AttnParams &p;
+    uint32_t ring;
+    int ent, ent_off;    // page and offset in it of this lane's key; of the tile's first key where page % TK == 0
+    uint32_t want;       // keys of the tile, a bit each
+
+    __device__ __forceinline__ Feed(const AttnParams &p_, uint32_t ring_) : p(p_), ring(ring_) {}
+
+    // Starts loading the entries of a tile of `n` (at most TK) keys from `key0` on; row: the request's table.
+    __device__ __forceinline__ void fetch(const int32_t *row, int key0, int n) {
+        const int lane = threadIdx.x & 31;
+        want = n < 32 ? (1u << n) - 1 : 0xffffffffu;
+        ent = -1;
+        if (p.one_page || lane < n) {
+            const int key = p.one_page ? key0 : key0 + lane;
+            const int blk = p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
+            ent_off = key - blk * p.page;
+            ent = row[blk];
+        }
+    }
+
+    // Starts the copies of the fetched tile into a stage; returns its valid keys.
+    __device__ __forceinline__ uint32_t tile(int stage, int64_t head_off) {
+        const int lane = threadIdx.x & 31;
+        const int sub = C::NCH >= 32 ? 0 : lane / C::NCH, ch0 = C::NCH >= 32 ? lane : lane % C::NCH;
+        const uint32_t ks = ring + stage * 2 * C::TILE_BYTES;
+        const bool has = ent >= 0 && ent < p.num_pages;
+        uint32_t valid = has ? want : 0u;
+        int64_t off = has ? ent * p.page_stride + ent_off * p.slot_stride + head_off : 0;
+        if (!p.one_page)
+            valid = __ballot_sync(0xffffffffu, has) & want;
+        if (valid != want && p.status)
+            atomicOr(p.status, 1);
+        if (p.one_page)
+            off += sub * p.slot_stride + ch0 * EPC;
+#pragma unroll
+        for (int j = 0; j < C::TK / RPI; j++) {
+            const int row = j * RPI + sub;
+            const int64_t ro = p.one_page ? off : __shfl_sync(0xffffffffu, off, row) + ch0 * EPC;
+            const bool ok = (valid >> row) & 1;
+#pragma unroll
+            for (int c = 0; c < CPL; c++) {
+                const int ch = ch0 + c * 32;
+                const bool in = ok && ch * EPC < p.D;
+                const int64_t at = in ? ro + c * 32 * EPC : 0;
+                const uint32_t d = ks + row * C::ROW_BYTES + ((ch ^ (row & 7)) << 4);
+                cp_async16(d, (const T *)p.k + at, in ? 16 : 0);
+                cp_async16(d + C::TILE_BYTES, (const T *)p.v + at, in ? 16 : 0);
+            }
+            if (p.one_page)
+                off += RPI * p.slot_stride;
+        }
+        return valid;
+    }
+
+    // Starts the copies of a segment's query rows into a stage; head(r) is row r's query head, or -1.
+    template <typename F>
+    __device__ __forceinline__ void query(int stage, int b, F head) {
+        const uint32_t qs = ring + stage * 2 * C::TILE_BYTES;
+        for (int i = threadIdx.x & 31; i < p.rows * C::NCH; i += 32) {
+            const int r = i / C::NCH, ch = i % C::NCH, h = head(r);
+            const bool in = h >= 0 && ch * EPC < p.D;
+            const T *src = (const T *)p.q + (in ? b * p.q_bs + h * p.q_hs + ch * EPC : 0);
+            cp_async16(qs + r * C::ROW_BYTES + ((ch ^ (r & 7)) << 4), src, in ? 16 : 0);
+        }
+    }
+};
+
 // A partial result in memory: rows x D outputs, then rows maxima, then rows sums
 // (relative to the maximum, as o is), to a multiple of 16 bytes.
 __host__ __device__ __forceinline__ int partial_floats(int rows, int D) { return (rows * (D + 2) + 3) / 4 * 4; }
@@ -522,6 +601,14 @@ __device__ __forceinline__ uint32_t range_at(uint32_t total, uint32_t n, uint32_
 __device__ __forceinline__ uint32_t range_of(uint32_t total, uint32_t n, uint32_t t) {
     const uint32_t q = total / n, r = total - q * n, cut = r * (q + 1);
     return t < cut ? t / (q + 1) : r + (t - cut) / q;
+}
+
+// Counts an arrival: what the CTA has written is visible to the CTA that counts
+// the last one (called by one thread, behind a barrier of its CTA).
+__device__ __forceinline__ uint32_t arrive(int *counter) {
+    uint32_t n;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(n) : "l"(counter) : "memory");
+    return n;
 }
 
 // A segment that more than one warp or CTA works on, as one CTA sees it.
@@ -552,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_kernel(con
     __shared__ uint32_t warp_sums[kWarps];
     __shared__ Chain chains[kWarps + 1];   // [0] the segment that the CTA's range begins inside of, [1 + w] opened by warp w
     __shared__ int last[2];
+    __shared__ int2 joins[2];
 
     pdl_wait();
     pdl_launch_dependents();
@@ -642,58 +730,21 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_kernel(con
         bool load_q = true, cur_q = true;         // the segment's query rows come first
         int len = min(p.lens[load.b], p.cap);
         int64_t head_off = (p.row_tiles == 1 ? load.seg : load.seg / p.row_tiles) * p.head_stride;
-        // the next tile's table entries, on the way while earlier tiles are issued: lane i holds key i
-        int ent = -1, ent_off = 0;
-        uint32_t want = 0;   // its keys, a bit each
+        Feed<C> feed(p, smem_u32(ring));
         auto fetch = [&]() {
-            const int key = (int)load.tile * C::TK + lane;
-            const int n = len - (int)load.tile * C::TK;
-            want = n < C::TK ? (1u << n) - 1 : C::TK == 32 ? 0xffffffffu : (1u << C::TK % 32) - 1;
-            ent = -1;
-            if (lane < C::TK && key < len) {
-                const int blk = p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
-                ent_off = key - blk * p.page;
-                ent = p.table[load.b * p.table_stride + blk];
-            }
+            int n = C::TK;
+            if (load.tile + 1 == load.tiles)
+                n = len - (int)load.tile * C::TK;
+            feed.fetch(p.table + load.b * p.table_stride, (int)load.tile * C::TK, n);
         };
         // Starts the copies of the next item (query rows or a tile) into a stage; the tile's valid keys.
         auto issue = [&](int stage) -> uint32_t {
-            const uint32_t ks = smem_u32(ring) + stage * 2 * C::TILE_BYTES, vs = ks + C::TILE_BYTES;
-            constexpr int EPC = 16 / (int)sizeof(T);                 // elements per chunk
             if (load_q) {
                 load_q = false;
-                for (int i = lane; i < p.rows * C::NCH; i += 32) {
-                    const int r = i / C::NCH, ch = i % C::NCH, e = ch * EPC;
-                    const int head = head_of(load.seg, r);
-                    const bool in = head >= 0 && e < p.D;
-                    const T *src = (const T *)p.q + (in ? load.b * p.q_bs + head * p.q_hs + e : 0);
-                    cp_async16(ks + r * C::ROW_BYTES + ((ch ^ (r & 7)) << 4), src, in ? 16 : 0);
-                }
+                feed.query(stage, load.b, [&](int r) { return head_of(load.seg, r); });
                 return 0;
             }
-            const bool has = ent >= 0 && ent < p.num_pages;
-            const uint32_t valid = __ballot_sync(0xffffffffu, has);
-            if (valid != want && p.status)
-                atomicOr(p.status, 1);
-            const int64_t off = has ? ent * p.page_stride + ent_off * p.slot_stride + head_off : 0;
-            constexpr int RPI = C::NCH >= 32 ? 1 : 32 / C::NCH;      // rows per instruction
-            constexpr int CPL = C::NCH > 32 ? C::NCH / 32 : 1;       // chunks of a row per lane
-            const int sub = C::NCH >= 32 ? 0 : lane / C::NCH, ch0 = C::NCH >= 32 ? lane : lane % C::NCH;
-#pragma unroll
-            for (int j = 0; j < C::TK / RPI; j++) {
-                const int row = j * RPI + sub;
-                const int64_t ro = __shfl_sync(0xffffffffu, off, row);
-                const bool ok = (valid >> row) & 1;
-#pragma unroll
-                for (int c = 0; c < CPL; c++) {
-                    const int ch = ch0 + c * 32, e = ch * EPC;
-                    const bool in = ok && e < p.D;
-                    const int64_t at = in ? ro + e : 0;
-                    const uint32_t d = row * C::ROW_BYTES + ((ch ^ (row & 7)) << 4);
-                    cp_async16(ks + d, (const T *)p.k + at, in ? 16 : 0);
-                    cp_async16(vs + d, (const T *)p.v + at, in ? 16 : 0);
-                }
-            }
+            const uint32_t valid = feed.tile(stage, head_off);
             if (--left > 0) {
                 const int b = load.b;
                 advance(sh, load);
@@ -767,8 +818,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_kernel(con
         store2(d + 2, o.z * inv, o.w * inv);
     };
 
-    // segments that cross warps: finished here, or this CTA's part of them to the workspace
-    const int n4 = p.rows * p.D / 4;
+    // segments that cross warps: finished here, or this CTA's part of them to the workspace; a warp per row
     bool wrote = false;
     for (int k = 0; k <= kWarps; k++) {
         const Chain ch = chains[k];
@@ -777,37 +827,40 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_kernel(con
         const bool whole = ch.first >= c0 && ch.end <= c1;
         float *dst = p.partials + ((int64_t)blockIdx.x * 2 + (k > 0)) * pf;
         wrote |= !whole;
-        for (int i = threadIdx.x; i < n4; i += kThreads) {
-            const int r = i * 4 / p.D, c = i * 4 - r * p.D;
-            float m[kWarps], M = -INFINITY;
+        for (int r = warp; r < p.rows; r += kWarps) {
+            const float *part[kWarps];
+            float w[kWarps], M = -INFINITY, l = 0.0f;
 #pragma unroll
             for (int j = 0; j < kWarps; j++) {
-                m[j] = j < ch.parts ? slot_of(ch.warp + j, k > 0 && j == 0)[p.rows * p.D + r] : -INFINITY;
-                M = fmaxf(M, m[j]);
+                part[j] = slot_of(ch.warp + min(j, ch.parts - 1), k > 0 && j == 0);
+                w[j] = j < ch.parts ? part[j][p.rows * p.D + r] : -INFINITY;
+                M = fmaxf(M, w[j]);
             }
             const float base = M == -INFINITY ? 0.0f : M;
-            float4 o = make_float4(0, 0, 0, 0);
-            float l = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kWarps; j++)
-                if (j < ch.parts) {
-                    const float *part = slot_of(ch.warp + j, k > 0 && j == 0);
-                    const float w = ex2(m[j] - base);
-                    fma4(o, w, *reinterpret_cast<const float4 *>(part + i * 4));
-                    l = fmaf(w, part[p.rows * p.D + p.rows + r], l);
-                }
-            if (whole) {
-                const int head = head_of(ch.seg, r);
-                if (head >= 0) {
-                    write4(ch.b, head, c, o, l > 0.0f ? 1.0f / l : 0.0f);
-                    if (c == 0 && p.lse)
-                        p.lse[(int64_t)ch.b * Hq + head] = lse_of(M, l * A::kSumScale);
-                }
-            } else {
-                *reinterpret_cast<float4 *>(dst + i * 4) = o;
-                if (c == 0) {
+            for (int j = 0; j < kWarps; j++) {
+                w[j] = ex2(w[j] - base);
+                l = fmaf(w[j], part[j][p.rows * p.D + p.rows + r], l);
+            }
+            const int head = whole ? head_of(ch.seg, r) : 0;
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            for (int c = lane * 4; c < p.D; c += 128) {
+                float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < kWarps; j++)
+                    if (j < ch.parts)
+                        fma4(o, w[j], *reinterpret_cast<const float4 *>(part[j] + r * p.D + c));
+                if (!whole)
+                    *reinterpret_cast<float4 *>(dst + r * p.D + c) = o;
+                else if (head >= 0)
+                    write4(ch.b, head, c, o, inv);
+            }
+            if (lane == 0) {
+                if (!whole) {
                     dst[p.rows * p.D + r] = M;
                     dst[p.rows * p.D + p.rows + r] = l;
+                } else if (head >= 0 && p.lse) {
+                    p.lse[(int64_t)ch.b * Hq + head] = lse_of(M, l * A::kSumScale);
                 }
             }
         }
@@ -816,7 +869,6 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_kernel(con
         return;
 
     // segments that cross CTAs: the CTA that arrives last joins the parts, in CTA order
-    __threadfence();
     __syncthreads();
     if (threadIdx.x < 2) {
         int mine = -1;
@@ -825,9 +877,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_kernel(con
             if (ch.parts == 0 || (ch.first >= c0 && ch.end <= c1))
                 continue;
             const uint32_t cf = range_of(total, nc, ch.first), cl = range_of(total, nc, ch.end - 1);
-            if ((uint32_t)atomicAdd(p.counters + cf, 1) == cl - cf) {
+            if (arrive(p.counters + cf) == cl - cf) {
                 p.counters[cf] = 0;
                 mine = k;
+                joins[threadIdx.x] = make_int2((int)cf, (int)(cl - cf) + 1);
             }
         }
         last[threadIdx.x] = mine;
@@ -837,135 +890,316 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_kernel(con
     for (int kind = 0; kind < 2; kind++) {
         if (last[kind] < 0)
             continue;
-        __threadfence();
         const Chain ch = chains[last[kind]];
-        const int cf = (int)range_of(total, nc, ch.first), np = (int)range_of(total, nc, ch.end - 1) - cf + 1;
+        const int cf = joins[kind].x, np = joins[kind].y;
         const float *first = p.partials + ((int64_t)cf * 2 + 1) * pf;             // part 0; part i at rest + (i - 1) * 2 pf
         const float *rest = p.partials + ((int64_t)cf + 1) * 2 * pf;
         auto part = [&](int i) { return i == 0 ? first : rest + (int64_t)(i - 1) * 2 * pf; };
-        // weights exp2(m_i - M) / sum, per row: [row][np]
-        float *wl = wm + p.rows * np, *red = wm + (2 * p.rows * np + 3) / 4 * 4;
-        for (int i = threadIdx.x; i < np * p.rows; i += kThreads) {
-            const int pi = i / p.rows, r = i - pi * p.rows;
-            const float *q = part(pi) + p.rows * p.D;
-            wm[r * np + pi] = __ldcg(q + r);
-            wl[r * np + pi] = __ldcg(q + p.rows + r);
-        }
-        __syncthreads();
-        for (int r = warp; r < p.rows; r += kWarps) {
+        // fewer rows than warps: 2^sh warps share a row and take every 2^sh-th part each
+        const int sh = p.rows == 1 ? 2 : p.rows == 2 ? 1 : 0, sets = 1 << sh;
+        static_assert(kWarps == 4, "sets of warps");
+        float *red = wm + (p.rows * (np + kWarps) + 3) / 4 * 4;                    // [sets][rows][D]
+        for (int r = warp >> sh; r < p.rows; r += kWarps >> sh) {
+            const int set = warp & (sets - 1);
+            float *w = wm + r * (np + kWarps) + set * ((np + sets - 1) >> sh);     // this set's weights
+            // the row's maximum and sum
             float M = -INFINITY, l = 0.0f;
-            for (int i = lane; i < np; i += 32)
-                M = fmaxf(M, wm[r * np + i]);
+            for (int i = lane; i < np; i += 32) {
+                const float mi = __ldcg(part(i) + p.rows * p.D + r), li = __ldcg(part(i) + p.rows * p.D + p.rows + r);
+                const float mn = fmaxf(M, mi), at = mn == -INFINITY ? 0.0f : mn;
+                l = l * ex2(M - at) + li * ex2(mi - at);
+                M = mn;
+                if ((i & (sets - 1)) == set)
+                    w[i >> sh] = mi;
+            }
+            const float mine = M;
 #pragma unroll
             for (int x = 16; x; x >>= 1)
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
             const float base = M == -INFINITY ? 0.0f : M;
-            for (int i = lane; i < np; i += 32) {
-                const float w = ex2(wm[r * np + i] - base);
-                wm[r * np + i] = w;
-                l = fmaf(w, wl[r * np + i], l);
-            }
+            l *= ex2(mine - base);
+            for (int i = lane; i < np; i += 32)   // the lane's own entries again
+                if ((i & (sets - 1)) == set)
+                    w[i >> sh] = ex2(w[i >> sh] - base);
 #pragma unroll
             for (int x = 16; x; x >>= 1)
                 l += __shfl_xor_sync(0xffffffffu, l, x);
             __syncwarp();
             const int head = head_of(ch.seg, r);
-            if (lane == 0) {
-                wl[r * np] = l > 0.0f ? 1.0f / l : 0.0f;
-                if (head >= 0 && p.lse)
-                    p.lse[(int64_t)ch.b * Hq + head] = lse_of(M, l * A::kSumScale);
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            for (int c = lane * 4; c < p.D; c += 128) {
+                float4 o = make_float4(0, 0, 0, 0);
+                for (int i0 = set; i0 < np; i0 += 8 * sets) {
+                    float4 v[8];   // eight loads on their way at a time
+#pragma unroll
+                    for (int u = 0; u < 8; u++)
+                        if (i0 + u * sets < np)
+                            v[u] = __ldcg(reinterpret_cast<const float4 *>(part(i0 + u * sets) + r * p.D + c));
+#pragma unroll
+                    for (int u = 0; u < 8; u++)
+                        if (i0 + u * sets < np)
+                            fma4(o, w[(i0 >> sh) + u], v[u]);
+                }
+                if (sets > 1)
+                    *reinterpret_cast<float4 *>(red + (set * p.rows + r) * p.D + c) = o;
+                else if (head >= 0)
+                    write4(ch.b, head, c, o, inv);
             }
-        }
-        __syncthreads();
-        // few outputs: `groups` sets of threads take every groups-th part each
-        int groups = 1;
-        while (groups < 8 && n4 * groups * 2 <= kThreads)
-            groups *= 2;
-        const int g = threadIdx.x / (kThreads / groups);
-        for (int i0 = 0; i0 < n4; i0 += kThreads / groups) {
-            const int i = i0 + (int)threadIdx.x % (kThreads / groups);
-            float4 o = make_float4(0, 0, 0, 0);
-            const int r = i * 4 / p.D, c = i * 4 - r * p.D;
-            if (i < n4) {
-#pragma unroll 8
-                for (int j = g; j < np; j += groups)
-                    fma4(o, wm[r * np + j], __ldcg(reinterpret_cast<const float4 *>(part(j) + i * 4)));
-            }
-            if (groups > 1) {   // n4 <= kThreads / groups: one round
-                if (g > 0 && i < n4)
-                    *reinterpret_cast<float4 *>(red + (g * n4 + i) * 4) = o;
+            if (lane == 0 && set == 0 && head >= 0 && p.lse)
+                p.lse[(int64_t)ch.b * Hq + head] = lse_of(M, l * A::kSumScale);
+            if (sets > 1) {   // one or two rows: every warp is here once
                 __syncthreads();
-                if (g == 0 && i < n4)
-                    for (int x = 1; x < groups; x++)
-                        fma4(o, 1.0f, *reinterpret_cast<const float4 *>(red + (x * n4 + i) * 4));
+                if (set == 0 && head >= 0)
+                    for (int c = lane * 4; c < p.D; c += 128) {
+                        float4 o = make_float4(0, 0, 0, 0);
+                        for (int x = 0; x < sets; x++)
+                            fma4(o, 1.0f, *reinterpret_cast<const float4 *>(red + (x * p.rows + r) * p.D + c));
+                        write4(ch.b, head, c, o, inv);
+                    }
             }
-            const int head = g == 0 && i < n4 ? head_of(ch.seg, r) : -1;
-            if (head >= 0)
-                write4(ch.b, head, c, o, wl[r * np]);
         }
         __syncthreads();
     }
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+
+// The same attention for calls that are too small to fill the GPU for long:
+// one cluster of S = 1, 2, 4 or 8 CTAs per segment, each CTA an S-th of its
+// tiles, every fourth of them to a warp.  No list, no workspace and no second
+// pass over memory: the parts are joined through distributed shared memory
+// behind one cluster barrier.
+template <typename C>
+__global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_cluster_kernel(const __grid_constant__ AttnParams p) {
+    using T = typename C::T;
+    using A = Acc<C, C::F16>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kRing = C::STAGES * 2 * C::TILE_BYTES;   // bytes a warp
+    const uint32_t ring = smem_u32(smem) + warp * kRing;
+    const uint32_t q_keep = smem_u32(smem) + kWarps * kRing + (C::F16 ? 0 : warp * p.rows * C::ROW_BYTES);
+    const int rank = blockIdx.x, S = gridDim.x, seg = blockIdx.y, b = blockIdx.z;
+    const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, r0 = (seg - h * p.row_tiles) * C::ROWS;
+    auto head_of = [&](int r) { return r0 + r < p.G ? h * p.G + r0 + r : -1; };
+
+    pdl_wait();
+    pdl_launch_dependents();
+    const int given = p.lens[b], len = min(max(given, 0), p.cap);
+    if (given != len && rank == 0 && seg == 0 && threadIdx.x == 0 && p.status)
+        atomicOr(p.status, 2);
+    const int tiles = (int)(((uint32_t)len + C::TK - 1) / C::TK);
+    const int per = (tiles + S - 1) >> p.split_shift;      // S = 1 << split_shift
+    const int end = min(tiles, (rank + 1) * per);
+    T *out = (T *)p.out + b * p.o_bs;
+    float *lse = p.lse ? p.lse + (int64_t)b * p.Hkv * p.G : nullptr;
+
+    A acc;
+    int t = rank * per + warp, load = t;   // tile to compute, tile to issue
+    const bool busy = t < end;
+    if (busy) {
+        const int32_t *row = p.table + b * p.table_stride;
+        const int64_t head_off = h * p.head_stride;
+        Feed<C> feed(p, ring);
+        feed.fetch(row, load * C::TK, min(C::TK, len - load * C::TK));
+        feed.query(0, b, head_of);
+        cp_commit();
+        uint32_t vmask[C::STAGES];   // valid keys of the tiles in flight, the oldest first
+        auto issue = [&](int stage) -> uint32_t {
+            const uint32_t valid = feed.tile(stage, head_off);
+            load += kWarps;
+            if (load < end)
+                feed.fetch(row, load * C::TK, min(C::TK, len - load * C::TK));
+            return valid;
+        };
+        vmask[0] = 0;
+#pragma unroll
+        for (int s = 1; s < C::STAGES; s++) {
+            vmask[s] = load < end ? issue(s) : 0u;
+            cp_commit();
+        }
+        cp_wait<C::STAGES - 1>();
+        __syncwarp();
+        acc.open(ring, q_keep, p.rows);
+        int stage = 0;
+        for (; t < end; t += kWarps) {
+            __syncwarp();   // every lane has read the stage that the last item left: it takes the next tile
+            const uint32_t nv = load < end ? issue(stage) : 0u;
+            cp_commit();
+            stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+            cp_wait<C::STAGES - 1>();
+            __syncwarp();
+#pragma unroll
+            for (int s = 0; s + 1 < C::STAGES; s++)
+                vmask[s] = vmask[s + 1];
+            vmask[C::STAGES - 1] = nv;
+            const uint32_t ks = ring + stage * 2 * C::TILE_BYTES;
+            acc.tile(ks, ks + C::TILE_BYTES, q_keep, p.rows, vmask[0], p.scale * kLog2e);
+        }
+        acc.finish();
+        __syncwarp();   // every lane has read the last tile of a ring that is written over
+        acc.to_slot(reinterpret_cast<float *>(smem + (size_t)warp * kRing), p.rows, p.D);
+    }
+    if (S > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+
+    // Joins: a warp per row and 128 outputs, over the ranks' warps; lane i looks after part i.
+    const int used = per > 0 ? (tiles + per - 1) / per : 0;   // ranks with a tile
+    const int last = tiles - (used - 1) * per;                // tiles of the last of them
+    const int np = used > 0 ? (used - 1) * min(per, kWarps) + min(last, kWarps) : 0;
+    const int in_rank = min(max(per, 1), kWarps);             // parts of every rank but the last
+    const int chunks = (p.D + 127) >> 7;
+    for (int task = warp * S + rank; task < p.rows * chunks; task += kWarps * S) {
+        const int r = chunks == 1 ? task : task >> 1, c = (chunks == 1 ? 0 : (task & 1) * 128) + lane * 4;
+        const int pr = lane / in_rank, pw = lane - pr * in_rank;
+        const uint32_t local = smem_u32(smem) + pw * kRing;
+        const uint32_t mine = S > 1 && lane < np ? cluster_map(local, pr) : local;
+        float m = -INFINITY, l = 0.0f;
+        if (lane < np) {
+            const uint32_t at = mine + (p.rows * p.D + r) * 4;
+            m = S > 1 ? ld_cluster(at) : *reinterpret_cast<float *>(smem + pw * kRing + (p.rows * p.D + r) * 4);
+            l = S > 1 ? ld_cluster(at + p.rows * 4)
+                      : *reinterpret_cast<float *>(smem + pw * kRing + (p.rows * p.D + p.rows + r) * 4);
+        }
+        float M = m;
+#pragma unroll
+        for (int x = 16; x; x >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        const float w = ex2(m - (M == -INFINITY ? 0.0f : M));
+        l *= w;
+#pragma unroll
+        for (int x = 16; x; x >>= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, x);
+        float4 o = make_float4(0, 0, 0, 0);
+        for (int i0 = 0; i0 < np; i0 += 4) {
+            float4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++) {   // a part behind the last: part 0 again, with weight 0
+                const int i = i0 + u < np ? i0 + u : 0;
+                const uint32_t at = __shfl_sync(0xffffffffu, mine, i) + (r * p.D + (c < p.D ? c : 0)) * 4;
+                v[u] = S > 1 ? ld_cluster4(at) : lds4(at);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const float wu = __shfl_sync(0xffffffffu, w, (i0 + u) & 31);
+                fma4(o, i0 + u < np ? wu : 0.0f, v[u]);
+            }
+        }
+        const int head = head_of(r);
+        if (head >= 0) {
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            if (c < p.D) {
+                T *d = out + head * p.o_hs + c;
+                store2(d, o.x * inv, o.y * inv);
+                store2(d + 2, o.z * inv, o.w * inv);
+            }
+            if (c == 0 && lse)
+                lse[head] = lse_of(M, l * A::kSumScale);
+        }
+    }
+    if (S > 1)
+        cluster_sync();   // no CTA leaves while another reads its parts
 }
 
 constexpr size_t kSmemMax = 227 * 1024 - 256;
 constexpr size_t kSmemSm = 228 * 1024;
 
+// Tuning hook: 0 = the rule in launch_cfg, 1 = always the list, 2 = always clusters.
+int g_mode = 0;
+
 template <typename C>
-int launch_cfg(const AttnParams &p, int most, size_t smem, unsigned flags, cudaStream_t s) {
-    static int cache[kMaxDevices] = {};
-    auto *kernel = paged_attention_kernel<C>;
-    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)smem, cache);
-    if (e != cudaSuccess)
-        return fail(MNB_ERR_CUDA, "mnb_paged_attention: %s", cudaGetErrorString(e));
-    const int by_smem = (int)(kSmemSm / (smem + 1024 + 256));
-    const int resident = device_sm_count() * (by_smem < C::kCtas ? by_smem : C::kCtas);
-    // the last join keeps two floats per row and part, and 16 bytes per thread, in the rings
-    const int joinable = (kWarps * C::STAGES * 2 * C::TILE_BYTES - kThreads * 16 - 16) / (8 * p.rows);
-    int grid = most < resident ? most : resident;
-    grid = grid < joinable ? grid : joinable;
+int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
+    static int caches[2][kMaxDevices] = {};
+    const int segs = p.Hkv * p.row_tiles;
+    p.one_page = p.page % C::TK == 0;
+    p.page_shift = (p.page & (p.page - 1)) == 0 ? __builtin_ctz((unsigned)p.page) : -1;
+    const int64_t most_tiles = (p.cap - 1) / C::TK + 1, tiles = most_tiles * p.B * segs;
+    if (tiles > 0x7fffffff)
+        return fail(MNB_ERR_SHAPE, "mnb_paged_attention: B=%d requests of up to %d tokens in %d heads are 2^31 tiles or more",
+                    p.B, p.cap, segs);
+    const size_t ring = (size_t)kWarps * (C::STAGES * 2 * C::TILE_BYTES + (C::F16 ? 0 : p.rows * C::ROW_BYTES));
+    const size_t list = ring + (size_t)kWarps * partial_floats(p.rows, p.D) * 4 + (size_t)(p.B + 1) * 4;
+    if (list > kSmemMax)
+        return fail(MNB_ERR_UNSUPPORTED, "mnb_paged_attention: %zu bytes of shared memory needed", list);
+    auto resident = [&](size_t smem) {
+        const int fit = (int)(kSmemSm / (smem + 1024 + 512));
+        return device_sm_count() * (fit < C::kCtas ? fit : C::kCtas);
+    };
+
+    // Clusters: as many CTAs a segment as the SMs have room for at once, but not more than a warp's tile each.
+    p.split_shift = 0;
+    while (p.split_shift < 3 && (int64_t)p.B * segs << (p.split_shift + 1) <= resident(ring) &&
+           (int64_t)kWarps << (p.split_shift + 1) <= most_tiles)
+        p.split_shift++;
+    const int64_t warp_tiles = (most_tiles - 1) / (kWarps << p.split_shift) + 1;
+    const bool clusters = g_mode == 2 || (g_mode == 0 && warp_tiles <= kClusterTiles);
+
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cudaLaunchAttribute attr[2];
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    if (flags & MNB_FLAG_PDL) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.numAttrs = 1;
-        cfg.attrs = attr;
+    cfg.attrs = attr;
+    if (clusters) {
+        cfg.gridDim = dim3(1u << p.split_shift, (unsigned)segs, (unsigned)p.B);
+        cfg.dynamicSmemBytes = ring;
+        if (p.split_shift) {
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << p.split_shift;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.numAttrs = 1;
+        }
+    } else {
+        // CTAs worth the table's width; the last join keeps a float per row and part, and an output row per warp,
+        // in the rings
+        const int64_t want = (tiles - 1) / p.min_tiles + 1;
+        const int joinable = (kWarps * (C::STAGES * 2 * C::TILE_BYTES - p.D * 4) - 32) / (4 * p.rows) - kWarps;
+        int grid = resident(list);
+        grid = grid < joinable ? grid : joinable;
+        cfg.gridDim = dim3((unsigned)(want < grid ? want : grid));
+        cfg.dynamicSmemBytes = list;
     }
-    e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (flags & MNB_FLAG_PDL) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    auto *kernel = clusters ? paged_attention_cluster_kernel<C> : paged_attention_kernel<C>;
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)cfg.dynamicSmemBytes, caches[clusters]);
+    if (e == cudaSuccess)
+        e = cudaLaunchKernelEx(&cfg, kernel, p);
     if (e != cudaSuccess)
         return fail(MNB_ERR_CUDA, "mnb_paged_attention: launch: %s", cudaGetErrorString(e));
     return MNB_OK;
 }
 
-// Shared memory of a CTA.
-template <typename C>
-size_t smem_bytes(int rows, int D, int B) {
-    return (size_t)kWarps * (C::STAGES * 2 * C::TILE_BYTES + (C::F16 ? 0 : rows * C::ROW_BYTES)) +
-           (size_t)kWarps * partial_floats(rows, D) * 4 + (size_t)(B + 1) * 4;
-}
-
 template <typename T, int DP, int ROWS>
-int launch_rows(const AttnParams &p, int most, unsigned flags, cudaStream_t s) {
-    using C = Cfg<T, DP, ROWS, 2>;
-    const size_t smem = smem_bytes<C>(p.rows, p.D, p.B);
-    if (smem > kSmemMax)
-        return fail(MNB_ERR_UNSUPPORTED, "mnb_paged_attention: %zu bytes of shared memory needed", smem);
-    return launch_cfg<C>(p, most, smem, flags, s);
+int launch_rows(const AttnParams &p, unsigned flags, cudaStream_t s) {
+    return launch_cfg<Cfg<T, DP, ROWS, 2>>(p, flags, s);
 }
 
 template <typename T, int DP>
-int launch_dp(const AttnParams &p, int ctas, unsigned flags, cudaStream_t s) {
+int launch_dp(const AttnParams &p, unsigned flags, cudaStream_t s) {
     if constexpr (std::is_same<T, half>::value)
-        return p.rows > 8 ? launch_rows<T, DP, 16>(p, ctas, flags, s) : launch_rows<T, DP, 8>(p, ctas, flags, s);
+        return p.rows > 8 ? launch_rows<T, DP, 16>(p, flags, s) : launch_rows<T, DP, 8>(p, flags, s);
     else
-        return p.rows > 4   ? launch_rows<T, DP, 8>(p, ctas, flags, s)
-               : p.rows > 2 ? launch_rows<T, DP, 4>(p, ctas, flags, s)
-               : p.rows > 1 ? launch_rows<T, DP, 2>(p, ctas, flags, s)
-                            : launch_rows<T, DP, 1>(p, ctas, flags, s);
+        return p.rows > 4   ? launch_rows<T, DP, 8>(p, flags, s)
+               : p.rows > 2 ? launch_rows<T, DP, 4>(p, flags, s)
+               : p.rows > 1 ? launch_rows<T, DP, 2>(p, flags, s)
+                            : launch_rows<T, DP, 1>(p, flags, s);
 }
 
 int rows_per_segment(int G, int f16) { return G < (f16 ? 16 : 8) ? G : (f16 ? 16 : 8); }
@@ -973,6 +1207,13 @@ int grid_of() { return device_sm_count() * kMaxCtas; }
 size_t counters_bytes() { return ((size_t)grid_of() * 4 + 127) / 128 * 128; }
 
 }  // namespace
+
+int set_paged_attention_mode(int mode) {
+    if (mode < 0 || mode > 2)
+        return MNB_ERR_INVALID_ARG;
+    g_mode = mode;
+    return MNB_OK;
+}
 
 size_t paged_attention_workspace_bytes(int Hq, int Hkv, int D, int f16) {
     return counters_bytes() + (size_t)grid_of() * 2 * partial_floats(rows_per_segment(Hq / Hkv, f16), D) * 4;
@@ -991,26 +1232,19 @@ int launch_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_
     p.rows = rows_per_segment(p.G, f16);
     p.row_tiles = (p.G + p.rows - 1) / p.rows;
     p.page = (int)c->page_size, p.num_pages = (int)c->num_pages, p.cap = max_blocks * p.page, p.scale = scale;
-    p.page_shift = (p.page & (p.page - 1)) == 0 ? __builtin_ctz((unsigned)p.page) : -1;
     p.min_tiles = kWarps;
     p.join_cost = (float)(p.rows * (p.D + 2) * 4) / (2 * (f16 ? 16 * 2 : 8 * 4) * p.D);   // bytes over bytes
     p.counters = (int *)workspace;
     p.partials = (float *)((uint8_t *)workspace + counters_bytes());
-    // no more CTAs than the table's width could need
-    const int tk = f16 ? 16 : 8;
-    const int64_t tiles = (int64_t)B * ((p.cap - 1) / tk + 1) * p.Hkv * p.row_tiles;
-    if (tiles > 0x7fffffff)
-        return fail(MNB_ERR_SHAPE, "mnb_paged_attention: B=%d requests of up to %d tokens in %d heads are 2^31 tiles or more",
-                    B, p.cap, p.Hkv * p.row_tiles);
-    const int64_t most = (tiles + p.min_tiles - 1) / p.min_tiles;
-    const int ctas = (int)(most < grid_of() ? (most < 1 ? 1 : most) : grid_of());
     if (f16)
-        return p.D <= 64    ? launch_dp<half, 64>(p, ctas, flags, s)
-               : p.D <= 128 ? launch_dp<half, 128>(p, ctas, flags, s)
-                            : launch_dp<half, 256>(p, ctas, flags, s);
-    return p.D <= 64    ? launch_dp<float, 64>(p, ctas, flags, s)
-           : p.D <= 128 ? launch_dp<float, 128>(p, ctas, flags, s)
-                        : launch_dp<float, 256>(p, ctas, flags, s);
+        return p.D <= 64    ? launch_dp<half, 64>(p, flags, s)
+               : p.D <= 128 ? launch_dp<half, 128>(p, flags, s)
+                            : launch_dp<half, 256>(p, flags, s);
+    return p.D <= 64    ? launch_dp<float, 64>(p, flags, s)
+           : p.D <= 128 ? launch_dp<float, 128>(p, flags, s)
+                        : launch_dp<float, 256>(p, flags, s);
 }
 
 }  // namespace mnb
+
+extern "C" MNB_API int mnb_tune_paged_attention(int mode) { return mnb::set_paged_attention_mode(mode); }

@@ -154,3 +154,8 @@ def test_binding_refuses_tensors(mnb):
         mnb.mnb_paged_tables(i, i, tab, 16, 3, i, i[:1], i, i, i, i, i[:1])
     with pytest.raises(mnb.MnbError, match="go together"):
         mnb.mnb_rope_append(None, q, q, kv, kv, i, None, None, None, q)
+
+
+def test_tuning_hook_checks_its_argument(mnb):
+    f = mnb._lib.mnb_tune_paged_attention
+    assert f(3) == INVALID and f(-1) == INVALID and f(0) == OK
