@@ -56,7 +56,8 @@ struct AttnParams {
     int one_page;                                          // a tile's keys are in one page: page % TK == 0
     int min_tiles;                                         // fewest tiles worth a CTA
     float join_cost;                                       // of a partial result in the last join, in tiles
-    int split_shift;                                       // cluster kernel: log2 of the CTAs per segment
+    uint32_t split_magic;                                  // cluster kernel: ceil(2^32 / CTAs per segment)
+    int stages;                                            // cluster kernel: of each warp's ring
     float scale;
 };
 
@@ -978,6 +979,18 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
     return r;
 }
 
+// Waits until at most n (1 .. kMaxStages - 1) groups of this thread's copies are on their way.
+__device__ __forceinline__ void cp_wait_rt(int n) {
+    switch (n) {
+    case 1: cp_wait<1>(); break;
+    case 2: cp_wait<2>(); break;
+    case 3: cp_wait<3>(); break;
+    case 4: cp_wait<4>(); break;
+    default: cp_wait<5>(); break;
+    }
+}
+constexpr int kMaxStages = 6;
+
 // The same attention for calls that are too small to fill the GPU for long:
 // one cluster of S = 1, 2, 4 or 8 CTAs per segment, each CTA an S-th of its
 // tiles, every fourth of them to a warp.  No list, no workspace and no second
@@ -989,9 +1002,10 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_cluster_ke
     using A = Acc<C, C::F16>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kRing = C::STAGES * 2 * C::TILE_BYTES;   // bytes a warp
+    const int kRing = p.stages * 2 * C::TILE_BYTES;   // bytes a warp
     const uint32_t ring = smem_u32(smem) + warp * kRing;
     const uint32_t q_keep = smem_u32(smem) + kWarps * kRing + (C::F16 ? 0 : warp * p.rows * C::ROW_BYTES);
+    __shared__ uint32_t vmask[kWarps][kMaxStages];    // valid keys of the tile in each stage
     const int rank = blockIdx.x, S = gridDim.x, seg = blockIdx.y, b = blockIdx.z;
     const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, r0 = (seg - h * p.row_tiles) * C::ROWS;
     auto head_of = [&](int r) { return r0 + r < p.G ? h * p.G + r0 + r : -1; };
@@ -1002,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_cluster_ke
     if (given != len && rank == 0 && seg == 0 && threadIdx.x == 0 && p.status)
         atomicOr(p.status, 2);
     const int tiles = (int)(((uint32_t)len + C::TK - 1) / C::TK);
-    const int per = (tiles + S - 1) >> p.split_shift;      // S = 1 << split_shift
+    const int per = S == 1 ? tiles : (int)__umulhi((uint32_t)(tiles + S - 1), p.split_magic);   // ceil(tiles / S)
     const int end = min(tiles, (rank + 1) * per);
     T *out = (T *)p.out + b * p.o_bs;
     float *lse = p.lse ? p.lse + (int64_t)b * p.Hkv * p.G : nullptr;
@@ -1017,37 +1031,33 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_cluster_ke
         feed.fetch(row, load * C::TK, min(C::TK, len - load * C::TK));
         feed.query(0, b, head_of);
         cp_commit();
-        uint32_t vmask[C::STAGES];   // valid keys of the tiles in flight, the oldest first
-        auto issue = [&](int stage) -> uint32_t {
+        auto issue = [&](int stage) {
             const uint32_t valid = feed.tile(stage, head_off);
+            if (lane == 0)
+                vmask[warp][stage] = valid;
             load += kWarps;
             if (load < end)
                 feed.fetch(row, load * C::TK, min(C::TK, len - load * C::TK));
-            return valid;
         };
-        vmask[0] = 0;
-#pragma unroll
-        for (int s = 1; s < C::STAGES; s++) {
-            vmask[s] = load < end ? issue(s) : 0u;
+        for (int s = 1; s < p.stages; s++) {
+            if (load < end)
+                issue(s);
             cp_commit();
         }
-        cp_wait<C::STAGES - 1>();
+        cp_wait_rt(p.stages - 1);
         __syncwarp();
         acc.open(ring, q_keep, p.rows);
         int stage = 0;
         for (; t < end; t += kWarps) {
             __syncwarp();   // every lane has read the stage that the last item left: it takes the next tile
-            const uint32_t nv = load < end ? issue(stage) : 0u;
+            if (load < end)
+                issue(stage);
             cp_commit();
-            stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-            cp_wait<C::STAGES - 1>();
+            stage = stage + 1 == p.stages ? 0 : stage + 1;
+            cp_wait_rt(p.stages - 1);
             __syncwarp();
-#pragma unroll
-            for (int s = 0; s + 1 < C::STAGES; s++)
-                vmask[s] = vmask[s + 1];
-            vmask[C::STAGES - 1] = nv;
             const uint32_t ks = ring + stage * 2 * C::TILE_BYTES;
-            acc.tile(ks, ks + C::TILE_BYTES, q_keep, p.rows, vmask[0], p.scale * kLog2e);
+            acc.tile(ks, ks + C::TILE_BYTES, q_keep, p.rows, vmask[warp][stage], p.scale * kLog2e);
         }
         acc.finish();
         __syncwarp();   // every lane has read the last tile of a ring that is written over
@@ -1120,7 +1130,7 @@ constexpr size_t kSmemMax = 227 * 1024 - 256;
 constexpr size_t kSmemSm = 228 * 1024;
 
 // Tuning hook: 0 = the rule in launch_cfg, 1 = always the list, 2 = always clusters.
-int g_mode = 0;
+int g_mode = 0, g_split = 0;
 
 template <typename C>
 int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
@@ -1142,11 +1152,13 @@ int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
     };
 
     // Clusters: as many CTAs a segment as the SMs have room for at once, but not more than a warp's tile each.
-    p.split_shift = 0;
-    while (p.split_shift < 3 && (int64_t)p.B * segs << (p.split_shift + 1) <= resident(ring) &&
-           (int64_t)kWarps << (p.split_shift + 1) <= most_tiles)
-        p.split_shift++;
-    const int64_t warp_tiles = (most_tiles - 1) / (kWarps << p.split_shift) + 1;
+    const int64_t all = (int64_t)p.B * segs;
+    int split = (int)(resident(ring) / all < 8 ? resident(ring) / all : 8);
+    const int64_t by_tiles = (most_tiles - 1) / kWarps + 1;
+    split = split < by_tiles ? split : (int)by_tiles;
+    split = g_split ? g_split : split < 1 ? 1 : split;
+    p.split_magic = split > 1 ? (uint32_t)((((uint64_t)1 << 32) + split - 1) / split) : 0;
+    const int64_t warp_tiles = (most_tiles - 1) / (kWarps * split) + 1;
     const bool clusters = g_mode == 2 || (g_mode == 0 && warp_tiles <= kClusterTiles);
 
     cudaLaunchConfig_t cfg = {};
@@ -1155,11 +1167,18 @@ int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     if (clusters) {
-        cfg.gridDim = dim3(1u << p.split_shift, (unsigned)segs, (unsigned)p.B);
-        cfg.dynamicSmemBytes = ring;
-        if (p.split_shift) {
+        // a deeper ring where the SMs have room for one
+        const int64_t ctas = all * split, sms = device_sm_count();
+        const int per_sm = ctas > sms * (C::kCtas - 1) ? C::kCtas : (int)((ctas - 1) / sms) + 1;
+        const size_t stage = (size_t)kWarps * 2 * C::TILE_BYTES, room = kSmemSm / per_sm - 1024 - 512;
+        const size_t q = ring - C::STAGES * stage;
+        const size_t fit = ((room < kSmemMax ? room : kSmemMax) - q) / stage;
+        p.stages = fit < 2 ? 2 : fit > kMaxStages ? kMaxStages : (int)fit;
+        cfg.gridDim = dim3((unsigned)split, (unsigned)segs, (unsigned)p.B);
+        cfg.dynamicSmemBytes = p.stages * stage + q;
+        if (split > 1) {
             attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 1u << p.split_shift;
+            attr[0].val.clusterDim.x = (unsigned)split;
             attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
             cfg.numAttrs = 1;
         }
@@ -1208,10 +1227,10 @@ size_t counters_bytes() { return ((size_t)grid_of() * 4 + 127) / 128 * 128; }
 
 }  // namespace
 
-int set_paged_attention_mode(int mode) {
-    if (mode < 0 || mode > 2)
+int set_paged_attention_mode(int mode, int split) {
+    if (mode < 0 || mode > 2 || split < 0 || split > 8)
         return MNB_ERR_INVALID_ARG;
-    g_mode = mode;
+    g_mode = mode, g_split = split;
     return MNB_OK;
 }
 
@@ -1247,4 +1266,6 @@ int launch_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_
 
 }  // namespace mnb
 
-extern "C" MNB_API int mnb_tune_paged_attention(int mode) { return mnb::set_paged_attention_mode(mode); }
+extern "C" MNB_API int mnb_tune_paged_attention(int mode, int split) {
+    return mnb::set_paged_attention_mode(mode, split);
+}
