@@ -35,9 +35,9 @@ MNB_API int mnb_tune_gemv_resident(int enable);
 
 /* mnb_paged_attention: which kernel runs -- 0 (default) by the call's sizes,
  * 1 the one that cuts the list of all tiles into equal ranges, 2 the one that
- * joins a segment's parts inside a cluster, of `split` CTAs (1..8; 0 = by the
- * call's sizes). */
-MNB_API int mnb_tune_paged_attention(int mode, int split);
+ * joins a segment's parts inside a cluster, of `split` CTAs (1..16) of `warps`
+ * warps (1..12; fewer where shared memory has no room); 0 = by the call's sizes. */
+MNB_API int mnb_tune_paged_attention(int mode, int split, int warps);
 
 /* Fault injection for tests of mnb_gemv_chain's timeout path (no GPU fault,
  * no hang): every later launch leaves task `task` uncounted, so the next task

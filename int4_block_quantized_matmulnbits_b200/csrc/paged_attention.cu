@@ -36,6 +36,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 3;   // per SM
+constexpr int kMaxWarps = 12; // of a CTA of the cluster kernel
 constexpr int kClusterTiles = 16;   // most tiles a warp of the cluster kernel may have
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -53,7 +54,7 @@ struct AttnParams {
     int64_t table_stride, page_stride, slot_stride, head_stride;
     int B, G, Hkv, D, rows, row_tiles, page, num_pages, cap;   // cap: rows the table has room for
     int page_shift;                                        // log2(page), -1 if it is no power of two
-    int one_page;                                          // a tile's keys are in one page: page % TK == 0
+    int one_page, whole;                                   // a tile's keys are in one page: page % TK == 0; and D == DP
     int min_tiles;                                         // fewest tiles worth a CTA
     float join_cost;                                       // of a partial result in the last join, in tiles
     uint32_t split_magic;                                  // cluster kernel: ceil(2^32 / CTAs per segment)
@@ -63,20 +64,27 @@ struct AttnParams {
 
 // Element type, padded head size, rows of query heads per segment.  A tile is
 // 8 KB of K and V (16 KB for heads of 256): 16 keys of 128 fp16 entries.
-template <typename T_, int DP_, int ROWS_, int STAGES_>
+// Rows are swizzled in shared memory (chunk ^ row % 8), so that reads of eight
+// rows' same chunk meet no bank twice.
+template <typename T_, int DP_, int ROWS_>
 struct Cfg {
     using T = T_;
     static constexpr bool F16 = std::is_same<T, half>::value;
-    static constexpr int DP = DP_, ROWS = ROWS_, STAGES = STAGES_;
+    static constexpr int DP = DP_, ROWS = ROWS_, STAGES = 2;
     static constexpr int TK = (F16 ? 16 : 8) * (DP <= 64 ? 2 : 1);   // keys per tile
     static constexpr int NCH = DP * (int)sizeof(T) / 16;             // 16-byte chunks per row
     static constexpr int ROW_BYTES = DP * (int)sizeof(T);
     static constexpr int TILE_BYTES = TK * ROW_BYTES;
+    static __device__ __forceinline__ uint32_t at(int row, int chunk) { return row * ROW_BYTES + (chunk ^ (row & 7)) * 16; }
+    static constexpr int kWarpsMost = DP > 128 ? 6 : kMaxWarps;      // as far as shared memory goes
     static constexpr int kCtas = DP > 128 ? 1 : !F16 && ROWS > 4 ? 2 : kMaxCtas;                          // CTAs on an SM, as far as registers go
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -201,13 +209,13 @@ struct Acc<C, true> {
             const int r = min(lane & 7, rows - 1);
 #pragma unroll
             for (int kk = 0; kk < KS; kk += 2)
-                ldsm4(qs + r * C::ROW_BYTES + (((kk * 2 + i) ^ (r & 7)) << 4), q[kk][0][0], q[kk][0][1], q[kk + 1][0][0],
+                ldsm4(qs + C::at(r, kk * 2 + i), q[kk][0][0], q[kk][0][1], q[kk + 1][0][0],
                       q[kk + 1][0][1]);
         } else {
             const int r = min((lane & 7) + (i >> 1) * 8, rows - 1);
 #pragma unroll
             for (int kk = 0; kk < KS; kk++)
-                ldsm4(qs + r * C::ROW_BYTES + (((kk * 2 + (i & 1)) ^ (r & 7)) << 4), q[kk][0][0], q[kk][0][1],
+                ldsm4(qs + C::at(r, kk * 2 + (i & 1)), q[kk][0][0], q[kk][0][1],
                       q[kk][NT - 1][0], q[kk][NT - 1][1]);
         }
 #pragma unroll
@@ -232,7 +240,7 @@ struct Acc<C, true> {
 #pragma unroll
                 for (int b = 0; b < KB; b++) {
                     uint32_t a0, a1, a2, a3;
-                    ldsm4(ks + (b * 16 + kr) * C::ROW_BYTES + (((kk * 2 + kc) ^ (kr & 7)) << 4), a0, a1, a2, a3);
+                    ldsm4(ks + C::at(b * 16 + kr, kk * 2 + kc), a0, a1, a2, a3);
 #pragma unroll
                     for (int t = 0; t < NT; t++)
                         mma16816(h[kk & 1][b][t], a0, a1, a2, a3, q[kk][t][0], q[kk][t][1]);
@@ -297,7 +305,7 @@ struct Acc<C, true> {
 #pragma unroll
             for (int b = 0; b < KB; b++) {
                 uint32_t a0, a1, a2, a3;
-                ldsm4t(vs + (b * 16 + vr) * C::ROW_BYTES + (((k * 2 + vc) ^ (vr & 7)) << 4), a0, a1, a2, a3);
+                ldsm4t(vs + C::at(b * 16 + vr, k * 2 + vc), a0, a1, a2, a3);
 #pragma unroll
                 for (int t = 0; t < NT; t++)
                     mma16816(o[k][t], a0, a1, a2, a3, p[b][t][0], p[b][t][1]);
@@ -374,10 +382,10 @@ struct Acc<C, false> {
     float4 o[C::ROWS][PER];
     float m[C::ROWS], l[C::ROWS];
 
-    // The segment's query rows, just landed at `land`: kept at `qs`.
+    // The segment's query rows, just landed at `land`: kept at `qs` (which may be `land`).
     __device__ __forceinline__ void open(uint32_t land, uint32_t qs, int rows) {
         __syncwarp();   // the last segment's rows have been read
-        for (int i = threadIdx.x & 31; i < rows * C::NCH; i += 32) {
+        for (int i = threadIdx.x & 31; land != qs && i < rows * C::NCH; i += 32) {
             const float4 v = lds4(land + i * 16);
             asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(qs + i * 16), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                          : "memory");
@@ -405,11 +413,11 @@ struct Acc<C, false> {
 #pragma unroll 4
         for (int c = 0; c < C::NCH / 4; c++) {
             const int ch = c * 4 + quarter;
-            const float4 k = lds4(ks + key * C::ROW_BYTES + ((ch ^ key) << 4));
+            const float4 k = lds4(ks + C::at(key, ch));
 #pragma unroll
             for (int r = 0; r < C::ROWS; r++) {
                 const int qr = min(r, rows - 1);
-                s[r] = dot(k, lds4(qs + qr * C::ROW_BYTES + ((ch ^ (qr & 7)) << 4)), s[r]);
+                s[r] = dot(k, lds4(qs + C::at(qr, ch)), s[r]);
             }
         }
         const bool ok = (valid >> key) & 1;
@@ -448,7 +456,7 @@ struct Acc<C, false> {
             float4 v[PER];
 #pragma unroll
             for (int c = 0; c < PER; c++)
-                v[c] = lds4(vs + kj * C::ROW_BYTES + (((col + c * 32) ^ kj) << 4));
+                v[c] = lds4(vs + C::at(kj, col + c * 32));
 #pragma unroll
             for (int r = 0; r < C::ROWS; r++) {
                 const float pr = __shfl_sync(0xffffffffu, s[r], kj);
@@ -522,6 +530,7 @@ struct Feed {
     static constexpr int EPC = 16 / (int)sizeof(T);                 // entries per chunk
     static constexpr int RPI = C::NCH >= 32 ? 1 : 32 / C::NCH;      // rows per instruction
     static constexpr int CPL = C::NCH > 32 ? C::NCH / 32 : 1;       // chunks of a row per lane
+    static constexpr uint32_t kAll = C::TK == 32 ? 0xffffffffu : (1u << C::TK % 32) - 1;
     const AttnParams &p;
     uint32_t ring;
     int ent, ent_off;    // page and offset in it of this lane's key; of the tile's first key where page % TK == 0
@@ -546,7 +555,9 @@ struct Feed {
     __device__ __forceinline__ uint32_t tile(int stage, int64_t head_off) {
         const int lane = threadIdx.x & 31;
         const int sub = C::NCH >= 32 ? 0 : lane / C::NCH, ch0 = C::NCH >= 32 ? lane : lane % C::NCH;
-        const uint32_t ks = ring + stage * 2 * C::TILE_BYTES;
+        // row j RPI + sub, chunk ch0 + 32 c: its swizzle is that of row sub but for the bits of j RPI
+        const uint32_t dst = ring + stage * 2 * C::TILE_BYTES + sub * C::ROW_BYTES;
+        const uint32_t sw = (ch0 ^ sub) << 4;
         const bool has = ent >= 0 && ent < p.num_pages;
         uint32_t valid = has ? want : 0u;
         int64_t off = has ? ent * p.page_stride + ent_off * p.slot_stride + head_off : 0;
@@ -554,24 +565,35 @@ struct Feed {
             valid = __ballot_sync(0xffffffffu, has) & want;
         if (valid != want && p.status)
             atomicOr(p.status, 1);
-        if (p.one_page)
-            off += sub * p.slot_stride + ch0 * EPC;
+        if (p.whole && valid == kAll) {   // one page, every key, every column
+            const T *k = (const T *)p.k + off + sub * p.slot_stride + ch0 * EPC;
+            const T *v = (const T *)p.v + off + sub * p.slot_stride + ch0 * EPC;
+            const int64_t step = RPI * p.slot_stride;
+#pragma unroll
+            for (int j = 0; j < C::TK / RPI; j++) {
+                const uint32_t d = dst + j * RPI * C::ROW_BYTES + (sw ^ ((j * RPI & 7) << 4));
+#pragma unroll
+                for (int c = 0; c < CPL; c++) {
+                    cp_async16(d + c * 512, k + c * 32 * EPC);
+                    cp_async16(d + c * 512 + C::TILE_BYTES, v + c * 32 * EPC);
+                }
+                k += step, v += step;
+            }
+            return valid;
+        }
 #pragma unroll
         for (int j = 0; j < C::TK / RPI; j++) {
             const int row = j * RPI + sub;
-            const int64_t ro = p.one_page ? off : __shfl_sync(0xffffffffu, off, row) + ch0 * EPC;
+            const int64_t ro = (p.one_page ? off + row * p.slot_stride : __shfl_sync(0xffffffffu, off, row)) + ch0 * EPC;
             const bool ok = (valid >> row) & 1;
+            const uint32_t d = dst + j * RPI * C::ROW_BYTES + (sw ^ ((j * RPI & 7) << 4));
 #pragma unroll
             for (int c = 0; c < CPL; c++) {
-                const int ch = ch0 + c * 32;
-                const bool in = ok && ch * EPC < p.D;
+                const bool in = ok && (ch0 + c * 32) * EPC < p.D;
                 const int64_t at = in ? ro + c * 32 * EPC : 0;
-                const uint32_t d = ks + row * C::ROW_BYTES + ((ch ^ (row & 7)) << 4);
-                cp_async16(d, (const T *)p.k + at, in ? 16 : 0);
-                cp_async16(d + C::TILE_BYTES, (const T *)p.v + at, in ? 16 : 0);
+                cp_async16(d + c * 512, (const T *)p.k + at, in ? 16 : 0);
+                cp_async16(d + c * 512 + C::TILE_BYTES, (const T *)p.v + at, in ? 16 : 0);
             }
-            if (p.one_page)
-                off += RPI * p.slot_stride;
         }
         return valid;
     }
@@ -584,7 +606,7 @@ struct Feed {
             const int r = i / C::NCH, ch = i % C::NCH, h = head(r);
             const bool in = h >= 0 && ch * EPC < p.D;
             const T *src = (const T *)p.q + (in ? b * p.q_bs + h * p.q_hs + ch * EPC : 0);
-            cp_async16(qs + r * C::ROW_BYTES + ((ch ^ (r & 7)) << 4), src, in ? 16 : 0);
+            cp_async16(qs + C::at(r, ch), src, in ? 16 : 0);
         }
     }
 };
@@ -980,6 +1002,7 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
 }
 
 // Waits until at most n (1 .. kMaxStages - 1) groups of this thread's copies are on their way.
+constexpr int kMaxStages = 6;
 __device__ __forceinline__ void cp_wait_rt(int n) {
     switch (n) {
     case 1: cp_wait<1>(); break;
@@ -989,23 +1012,22 @@ __device__ __forceinline__ void cp_wait_rt(int n) {
     default: cp_wait<5>(); break;
     }
 }
-constexpr int kMaxStages = 6;
 
-// The same attention for calls that are too small to fill the GPU for long:
-// one cluster of S = 1, 2, 4 or 8 CTAs per segment, each CTA an S-th of its
-// tiles, every fourth of them to a warp.  No list, no workspace and no second
-// pass over memory: the parts are joined through distributed shared memory
-// behind one cluster barrier.
+// The same attention with one cluster of S CTAs per segment: a CTA has an S-th
+// of the segment's tiles, W warps take every W-th of them.  No list, no
+// workspace and no second pass over memory: the parts are joined in shared
+// memory, then through distributed shared memory behind one cluster barrier.
 template <typename C>
-__global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_cluster_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_cluster_kernel(const __grid_constant__ AttnParams p) {
     using T = typename C::T;
     using A = Acc<C, C::F16>;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ uint32_t vmask[kMaxWarps][kMaxStages];    // valid keys of the tile in each stage
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int kRing = p.stages * 2 * C::TILE_BYTES;   // bytes a warp
-    const uint32_t ring = smem_u32(smem) + warp * kRing;
-    const uint32_t q_keep = smem_u32(smem) + kWarps * kRing + (C::F16 ? 0 : warp * p.rows * C::ROW_BYTES);
-    __shared__ uint32_t vmask[kWarps][kMaxStages];    // valid keys of the tile in each stage
+    uint8_t *my_ring = smem + (size_t)warp * kRing;
+    const uint32_t ring = smem_u32(my_ring);
+    uint8_t *q_rows = smem + (size_t)W * kRing;
     const int rank = blockIdx.x, S = gridDim.x, seg = blockIdx.y, b = blockIdx.z;
     const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, r0 = (seg - h * p.row_tiles) * C::ROWS;
     auto head_of = [&](int r) { return r0 + r < p.G ? h * p.G + r0 + r : -1; };
@@ -1021,72 +1043,64 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_cluster_ke
     T *out = (T *)p.out + b * p.o_bs;
     float *lse = p.lse ? p.lse + (int64_t)b * p.Hkv * p.G : nullptr;
 
-    A acc;
+    const int32_t *row = p.table + b * p.table_stride;
+    const int64_t head_off = h * p.head_stride;
     int t = rank * per + warp, load = t;   // tile to compute, tile to issue
-    const bool busy = t < end;
-    if (busy) {
-        const int32_t *row = p.table + b * p.table_stride;
-        const int64_t head_off = h * p.head_stride;
-        Feed<C> feed(p, ring);
-        feed.fetch(row, load * C::TK, min(C::TK, len - load * C::TK));
-        feed.query(0, b, head_of);
-        cp_commit();
-        auto issue = [&](int stage) {
+    Feed<C> feed(p, ring);
+    auto issue = [&](int stage) {
+        if (load < end) {
             const uint32_t valid = feed.tile(stage, head_off);
             if (lane == 0)
                 vmask[warp][stage] = valid;
-            load += kWarps;
+            load += W;
             if (load < end)
                 feed.fetch(row, load * C::TK, min(C::TK, len - load * C::TK));
-        };
-        for (int s = 1; s < p.stages; s++) {
-            if (load < end)
-                issue(s);
-            cp_commit();
         }
-        cp_wait_rt(p.stages - 1);
-        __syncwarp();
-        acc.open(ring, q_keep, p.rows);
+        cp_commit();
+    };
+    if (load < end)
+        feed.fetch(row, load * C::TK, min(C::TK, len - load * C::TK));
+    for (int s = 0; s + 1 < p.stages; s++)
+        issue(s);
+    // the segment's query rows, for all warps
+    for (int i = threadIdx.x; i < p.rows * C::NCH; i += blockDim.x) {
+        const int r = i / C::NCH, ch = i % C::NCH, head = head_of(r);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (head >= 0 && ch * (16 / (int)sizeof(T)) < p.D)
+            v = ldg_v4((const T *)p.q + b * p.q_bs + head * p.q_hs + ch * (16 / (int)sizeof(T)));
+        *reinterpret_cast<uint4 *>(q_rows + C::at(r, ch)) = v;
+    }
+    __syncthreads();
+
+    A acc;
+    if (t < end) {
+        const uint32_t qs = smem_u32(q_rows);
+        acc.open(qs, qs, p.rows);
         int stage = 0;
-        for (; t < end; t += kWarps) {
-            __syncwarp();   // every lane has read the stage that the last item left: it takes the next tile
-            if (load < end)
-                issue(stage);
-            cp_commit();
-            stage = stage + 1 == p.stages ? 0 : stage + 1;
+        for (; t < end; t += W) {
+            __syncwarp();   // every lane has read the stage that the last tile left: it takes the next one
+            issue(stage == 0 ? p.stages - 1 : stage - 1);
             cp_wait_rt(p.stages - 1);
             __syncwarp();
             const uint32_t ks = ring + stage * 2 * C::TILE_BYTES;
-            acc.tile(ks, ks + C::TILE_BYTES, q_keep, p.rows, vmask[warp][stage], p.scale * kLog2e);
+            acc.tile(ks, ks + C::TILE_BYTES, qs, p.rows, vmask[warp][stage], p.scale * kLog2e);
+            stage = stage + 1 == p.stages ? 0 : stage + 1;
         }
         acc.finish();
-        __syncwarp();   // every lane has read the last tile of a ring that is written over
-        acc.to_slot(reinterpret_cast<float *>(smem + (size_t)warp * kRing), p.rows, p.D);
+        __syncwarp();
+        acc.to_slot(reinterpret_cast<float *>(my_ring), p.rows, p.D);
     }
-    if (S > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+    __syncthreads();
 
-    // Joins: a warp per row and 128 outputs, over the ranks' warps; lane i looks after part i.
-    const int used = per > 0 ? (tiles + per - 1) / per : 0;   // ranks with a tile
-    const int last = tiles - (used - 1) * per;                // tiles of the last of them
-    const int np = used > 0 ? (used - 1) * min(per, kWarps) + min(last, kWarps) : 0;
-    const int in_rank = min(max(per, 1), kWarps);             // parts of every rank but the last
-    const int chunks = (p.D + 127) >> 7;
-    for (int task = warp * S + rank; task < p.rows * chunks; task += kWarps * S) {
+    // The CTA's warps joined: a warp per row and 128 outputs, lane i looks after warp i.
+    const int chunks = (p.D + 127) >> 7, tasks = p.rows * chunks;
+    const int parts = min(max(end - rank * per, 0), W);
+    float *cta_part = reinterpret_cast<float *>(smem) + partial_floats(p.rows, p.D);   // in warp 0's ring, behind its part
+    for (int task = warp; task < tasks; task += W) {
         const int r = chunks == 1 ? task : task >> 1, c = (chunks == 1 ? 0 : (task & 1) * 128) + lane * 4;
-        const int pr = lane / in_rank, pw = lane - pr * in_rank;
-        const uint32_t local = smem_u32(smem) + pw * kRing;
-        const uint32_t mine = S > 1 && lane < np ? cluster_map(local, pr) : local;
-        float m = -INFINITY, l = 0.0f;
-        if (lane < np) {
-            const uint32_t at = mine + (p.rows * p.D + r) * 4;
-            m = S > 1 ? ld_cluster(at) : *reinterpret_cast<float *>(smem + pw * kRing + (p.rows * p.D + r) * 4);
-            l = S > 1 ? ld_cluster(at + p.rows * 4)
-                      : *reinterpret_cast<float *>(smem + pw * kRing + (p.rows * p.D + p.rows + r) * 4);
-        }
-        float M = m;
+        const float *ml = reinterpret_cast<const float *>(smem + (size_t)lane * kRing) + p.rows * p.D + r;
+        const float m = lane < parts ? ml[0] : -INFINITY;
+        float l = lane < parts ? ml[p.rows] : 0.0f, M = m;
 #pragma unroll
         for (int x = 16; x; x >>= 1)
             M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
@@ -1096,47 +1110,92 @@ __global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_cluster_ke
         for (int x = 16; x; x >>= 1)
             l += __shfl_xor_sync(0xffffffffu, l, x);
         float4 o = make_float4(0, 0, 0, 0);
-        for (int i0 = 0; i0 < np; i0 += 4) {
-            float4 v[4];
-#pragma unroll
-            for (int u = 0; u < 4; u++) {   // a part behind the last: part 0 again, with weight 0
-                const int i = i0 + u < np ? i0 + u : 0;
-                const uint32_t at = __shfl_sync(0xffffffffu, mine, i) + (r * p.D + (c < p.D ? c : 0)) * 4;
-                v[u] = S > 1 ? ld_cluster4(at) : lds4(at);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const float wu = __shfl_sync(0xffffffffu, w, (i0 + u) & 31);
-                fma4(o, i0 + u < np ? wu : 0.0f, v[u]);
-            }
+#pragma unroll 4
+        for (int i = 0; i < parts; i++) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            if (c < p.D)
+                fma4(o, wi, *reinterpret_cast<const float4 *>(smem + (size_t)i * kRing + (r * p.D + c) * 4));
         }
-        const int head = head_of(r);
-        if (head >= 0) {
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            if (c < p.D) {
-                T *d = out + head * p.o_hs + c;
-                store2(d, o.x * inv, o.y * inv);
-                store2(d + 2, o.z * inv, o.w * inv);
+        if (S > 1) {
+            if (c < p.D)
+                *reinterpret_cast<float4 *>(cta_part + r * p.D + c) = o;
+            if (c == 0) {
+                cta_part[p.rows * p.D + r] = M;
+                cta_part[p.rows * p.D + p.rows + r] = l;
             }
-            if (c == 0 && lse)
-                lse[head] = lse_of(M, l * A::kSumScale);
+        } else {
+            const int head = head_of(r);
+            if (head >= 0) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                if (c < p.D) {
+                    T *d = out + head * p.o_hs + c;
+                    store2(d, o.x * inv, o.y * inv);
+                    store2(d + 2, o.z * inv, o.w * inv);
+                }
+                if (c == 0 && lse)
+                    lse[head] = lse_of(M, l * A::kSumScale);
+            }
         }
     }
-    if (S > 1)
-        cluster_sync();   // no CTA leaves while another reads its parts
+    if (S > 1) {
+        cluster_sync();
+        // the ranks joined, the same way; lane i looks after rank i
+        const int used = per > 0 ? (tiles + per - 1) / per : 0;   // ranks with a tile
+        const uint32_t mine = cluster_map(smem_u32(cta_part), lane < used ? lane : rank);
+        for (int task = warp * S + rank; task < tasks; task += W * S) {
+            const int r = chunks == 1 ? task : task >> 1, c = (chunks == 1 ? 0 : (task & 1) * 128) + lane * 4;
+            const uint32_t ml = mine + (p.rows * p.D + r) * 4;
+            const float m = lane < used ? ld_cluster(ml) : -INFINITY;
+            float l = lane < used ? ld_cluster(ml + p.rows * 4) : 0.0f, M = m;
+            float4 v[8];
+            const uint32_t at = (r * p.D + (c < p.D ? c : 0)) * 4;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const uint32_t part = __shfl_sync(0xffffffffu, mine, i);
+                v[i] = i < used ? ld_cluster4(part + at) : make_float4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int x = 16; x; x >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+            const float w = ex2(m - (M == -INFINITY ? 0.0f : M));
+            l *= w;
+#pragma unroll
+            for (int x = 16; x; x >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, x);
+            float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                fma4(o, __shfl_sync(0xffffffffu, w, i), v[i]);
+            for (int i = 8; i < used; i++)
+                fma4(o, __shfl_sync(0xffffffffu, w, i), ld_cluster4(__shfl_sync(0xffffffffu, mine, i) + at));
+            const int head = head_of(r);
+            if (head >= 0) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                if (c < p.D) {
+                    T *d = out + head * p.o_hs + c;
+                    store2(d, o.x * inv, o.y * inv);
+                    store2(d + 2, o.z * inv, o.w * inv);
+                }
+                if (c == 0 && lse)
+                    lse[head] = lse_of(M, l * A::kSumScale);
+            }
+        }
+        cluster_sync();   // no CTA leaves while another reads its part
+    }
 }
 
 constexpr size_t kSmemMax = 227 * 1024 - 256;
 constexpr size_t kSmemSm = 228 * 1024;
 
 // Tuning hook: 0 = the rule in launch_cfg, 1 = always the list, 2 = always clusters.
-int g_mode = 0, g_split = 0;
+int g_mode = 0, g_split = 0, g_warps = 0;
 
 template <typename C>
 int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
     static int caches[2][kMaxDevices] = {};
     const int segs = p.Hkv * p.row_tiles;
     p.one_page = p.page % C::TK == 0;
+    p.whole = p.one_page && p.D == C::DP;
     p.page_shift = (p.page & (p.page - 1)) == 0 ? __builtin_ctz((unsigned)p.page) : -1;
     const int64_t most_tiles = (p.cap - 1) / C::TK + 1, tiles = most_tiles * p.B * segs;
     if (tiles > 0x7fffffff)
@@ -1151,14 +1210,19 @@ int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
         return device_sm_count() * (fit < C::kCtas ? fit : C::kCtas);
     };
 
-    // Clusters: as many CTAs a segment as the SMs have room for at once, but not more than a warp's tile each.
+    // Clusters.
     const int64_t all = (int64_t)p.B * segs;
-    int split = (int)(resident(ring) / all < 8 ? resident(ring) / all : 8);
+    const size_t per_warp = (size_t)C::TILE_BYTES * 2, q_bytes = (size_t)p.rows * C::ROW_BYTES;
+    int split = (int)(resident(kWarps * 2 * per_warp + q_bytes) / all < 8 ? resident(kWarps * 2 * per_warp + q_bytes) / all : 8);
     const int64_t by_tiles = (most_tiles - 1) / kWarps + 1;
     split = split < by_tiles ? split : (int)by_tiles;
     split = g_split ? g_split : split < 1 ? 1 : split;
+    int warps = g_warps ? g_warps : kWarps;
+    const int fit_warps = (int)((kSmemMax - q_bytes) / (2 * per_warp));
+    warps = warps < fit_warps ? warps : fit_warps;
+    warps = warps < C::kWarpsMost ? warps : C::kWarpsMost;
     p.split_magic = split > 1 ? (uint32_t)((((uint64_t)1 << 32) + split - 1) / split) : 0;
-    const int64_t warp_tiles = (most_tiles - 1) / (kWarps * split) + 1;
+    const int64_t warp_tiles = (most_tiles - 1) / (warps * split) + 1;
     const bool clusters = g_mode == 2 || (g_mode == 0 && warp_tiles <= kClusterTiles);
 
     cudaLaunchConfig_t cfg = {};
@@ -1169,13 +1233,14 @@ int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
     if (clusters) {
         // a deeper ring where the SMs have room for one
         const int64_t ctas = all * split, sms = device_sm_count();
-        const int per_sm = ctas > sms * (C::kCtas - 1) ? C::kCtas : (int)((ctas - 1) / sms) + 1;
-        const size_t stage = (size_t)kWarps * 2 * C::TILE_BYTES, room = kSmemSm / per_sm - 1024 - 512;
-        const size_t q = ring - C::STAGES * stage;
-        const size_t fit = ((room < kSmemMax ? room : kSmemMax) - q) / stage;
+        const int most_ctas = kMaxWarps / warps;
+        const int per_sm = ctas > sms * (most_ctas - 1) ? most_ctas : (int)((ctas - 1) / sms) + 1;
+        const size_t room = kSmemSm / per_sm - 1024 - 1024;
+        const size_t fit = ((room < kSmemMax ? room : kSmemMax) - q_bytes) / (warps * per_warp);
         p.stages = fit < 2 ? 2 : fit > kMaxStages ? kMaxStages : (int)fit;
+        cfg.blockDim = dim3((unsigned)warps * 32);
         cfg.gridDim = dim3((unsigned)split, (unsigned)segs, (unsigned)p.B);
-        cfg.dynamicSmemBytes = p.stages * stage + q;
+        cfg.dynamicSmemBytes = p.stages * warps * per_warp + q_bytes;
         if (split > 1) {
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = (unsigned)split;
@@ -1198,6 +1263,8 @@ int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
     }
     auto *kernel = clusters ? paged_attention_cluster_kernel<C> : paged_attention_kernel<C>;
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)cfg.dynamicSmemBytes, caches[clusters]);
+    if (e == cudaSuccess && clusters && split > 8)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess)
         e = cudaLaunchKernelEx(&cfg, kernel, p);
     if (e != cudaSuccess)
@@ -1207,7 +1274,7 @@ int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
 
 template <typename T, int DP, int ROWS>
 int launch_rows(const AttnParams &p, unsigned flags, cudaStream_t s) {
-    return launch_cfg<Cfg<T, DP, ROWS, 2>>(p, flags, s);
+    return launch_cfg<Cfg<T, DP, ROWS>>(p, flags, s);
 }
 
 template <typename T, int DP>
@@ -1227,10 +1294,10 @@ size_t counters_bytes() { return ((size_t)grid_of() * 4 + 127) / 128 * 128; }
 
 }  // namespace
 
-int set_paged_attention_mode(int mode, int split) {
-    if (mode < 0 || mode > 2 || split < 0 || split > 8)
+int set_paged_attention_mode(int mode, int split, int warps) {
+    if (mode < 0 || mode > 2 || split < 0 || split > 16 || warps < 0 || warps > kMaxWarps)
         return MNB_ERR_INVALID_ARG;
-    g_mode = mode, g_split = split;
+    g_mode = mode, g_split = split, g_warps = warps;
     return MNB_OK;
 }
 
@@ -1266,6 +1333,6 @@ int launch_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_
 
 }  // namespace mnb
 
-extern "C" MNB_API int mnb_tune_paged_attention(int mode, int split) {
-    return mnb::set_paged_attention_mode(mode, split);
+extern "C" MNB_API int mnb_tune_paged_attention(int mode, int split, int warps) {
+    return mnb::set_paged_attention_mode(mode, split, warps);
 }

@@ -197,13 +197,15 @@ def test_append_keys_and_values_alone(mnb, cuda_dev):
 
 # ---------------------------------------------------------------- attention
 
-@pytest.fixture(params=["by_sizes", "list", "clusters", "clusters of 1", "clusters of 5"])
+@pytest.fixture(params=["by_sizes", "list", "1x4", "2x12", "5x3", "8x4"])
 def kernel(mnb, request):
-    """Each test with the kernel that the sizes choose, and with either of the two."""
+    """Each test with the kernel that the sizes choose, with the one that cuts a list, and with clusters of
+    (CTAs)x(warps)."""
     mode = dict(by_sizes=0, list=1).get(request.param, 2)
-    assert mnb._lib.mnb_tune_paged_attention(mode, int(request.param[-1]) if request.param[-1].isdigit() else 0) == 0
+    split, warps = map(int, request.param.split("x")) if mode == 2 else (0, 0)
+    assert mnb._lib.mnb_tune_paged_attention(mode, split, warps) == 0
     yield request.param
-    mnb._lib.mnb_tune_paged_attention(0, 0)
+    mnb._lib.mnb_tune_paged_attention(0, 0, 0)
 
 
 def run_attn(mnb, dev, case, scale, ws=None, lse=True, status=None):

@@ -158,4 +158,5 @@ def test_binding_refuses_tensors(mnb):
 
 def test_tuning_hook_checks_its_argument(mnb):
     f = mnb._lib.mnb_tune_paged_attention
-    assert f(3, 0) == INVALID and f(-1, 0) == INVALID and f(2, 9) == INVALID and f(0, 0) == OK
+    assert f(3, 0, 0) == INVALID and f(-1, 0, 0) == INVALID and f(2, 17, 0) == INVALID and f(2, 0, 13) == INVALID
+    assert f(0, 0, 0) == OK
