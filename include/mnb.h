@@ -452,8 +452,7 @@ MNB_API int mnb_rope_append(const void *q, int64_t q_token_stride, int64_t q_hea
  * left out (bit 0).  Nothing behind a request's n tokens is read: entries of
  * the block table and rows of its last page there may hold anything.
  *   lse fp32 [B][Hq] or NULL.  1 <= Hq <= 4096, Hq % Hkv == 0, 0 <= B <= 4096,
- *   max_blocks * page_size <= 2^31 - 64, and B * Hq * max_blocks * page_size
- *   below 2^34 (MNB_ERR_SHAPE may come later, where heads share).
+ *   max_blocks * page_size <= 2^31 - 64.
  *   Results are the same, bit for bit, from call to call on one GPU model.
  * workspace: mnb_paged_attention_workspace_bytes (for the current device),
  * 16-byte aligned, ZERO-FILLED before its first use; its first bytes count

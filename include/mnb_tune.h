@@ -33,11 +33,10 @@ MNB_API int mnb_tune_gemv_split(int w, int s);
  * it; 0 runs the general decode kernel. */
 MNB_API int mnb_tune_gemv_resident(int enable);
 
-/* mnb_paged_attention: which kernel runs -- 0 (default) by the call's sizes,
- * 1 the one that cuts the list of all tiles into equal ranges, 2 the one that
- * joins a segment's parts inside a cluster, of `split` CTAs (1..16) of `warps`
- * warps (1..12; fewer where shared memory has no room); 0 = by the call's sizes. */
-MNB_API int mnb_tune_paged_attention(int mode, int split, int warps);
+/* mnb_paged_attention: the CTAs of a cluster (1..8), the warps of a CTA (1..12;
+ * 6 is the most for heads above 128) and the clusters per segment (1..32; one
+ * where a call has more than 64 in all); 0 = by the call's sizes. */
+MNB_API int mnb_tune_paged_attention(int split, int warps, int groups);
 
 /* Fault injection for tests of mnb_gemv_chain's timeout path (no GPU fault,
  * no hang): every later launch leaves task `task` uncounted, so the next task

@@ -9,21 +9,19 @@
 // Two such (m, l, o) over disjoint keys join the same way, so the cache's
 // length may be cut anywhere.
 //
-// Work split.  The keys of every (request, KV head, row tile of query heads) --
-// a segment -- are cut into tiles of TK keys.  All tiles of the call, in the
-// order (request, segment, tile), form one list that is cut into equal
-// contiguous ranges, one per CTA, and each CTA's range again into one per warp:
-// every warp streams the same number of tiles (+-1) whatever the lengths are.
-// A segment inside one warp's range is finished there; one that crosses warps
-// is joined in shared memory, one that crosses CTAs through the workspace, by
-// the CTA that arrives last, in CTA order (the result does not depend on which
-// CTA that is).
+// Work split.  The keys of a segment -- a (request, KV head, row tile of query
+// heads) -- are cut into tiles of TK keys: first over P groups, then over the S
+// CTAs of each group's thread-block cluster, then every W-th tile to each of a
+// CTA's W warps.  The parts are joined in that order's reverse: the warps' in
+// shared memory, the cluster's through distributed shared memory behind one
+// cluster barrier, the groups' (P > 1 only where a few long segments would leave
+// most SMs idle) through the workspace, by the group that arrives last, in group
+// order, so that no result depends on which group that is.
 //
-// Each warp owns a ring of STAGES tiles in shared memory that it fills with
-// 16-byte cp.async (rows behind the length and rows of page ids outside the
-// pool are zero-filled and masked, never read) and drains by itself: the main
-// loop has no CTA barrier, and the next segment's query rows (a stage of their
-// own) and first tiles are in flight while the current one ends.
+// Each warp owns a ring of tiles in shared memory that it fills with 16-byte
+// cp.async (rows behind the length and rows of page ids outside the pool are
+// zero-filled and masked, never read) and drains by itself: the main loop has no
+// CTA barrier, and a warp waits for its own copies only.
 #include <type_traits>
 
 #include "common.cuh"
@@ -33,32 +31,44 @@
 namespace mnb {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCtas = 3;   // per SM
-constexpr int kMaxWarps = 12; // of a CTA of the cluster kernel
-constexpr int kClusterTiles = 16;   // most tiles a warp of the cluster kernel may have
+constexpr int kMaxSplit = 8;    // CTAs of a cluster
+constexpr int kMaxWarps = 12;   // of a CTA
+constexpr int kMaxStages = 6;   // of a warp's ring
+constexpr int kMaxGroups = 64;  // of a call that has more than one per segment
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// Division of a number below 2^31 by an invariant one: Granlund and Montgomery,
+// "Division by Invariant Integers using Multiplication" (1994), figure 4.1.
+struct Div {
+    uint32_t m;
+    int sh1, sh2;
+};
+Div div_by(uint32_t d) {
+    int l = 0;
+    while (((uint64_t)1 << l) < d)
+        l++;
+    return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l < 1 ? l : 1, l > 1 ? l - 1 : 0};
+}
+__device__ __forceinline__ int quotient(int n, const Div &d) {
+    const uint32_t t = __umulhi(d.m, (uint32_t)n);
+    return (int)((t + (((uint32_t)n - t) >> d.sh1)) >> d.sh2);
+}
 
 struct AttnParams {
     const void *q, *k, *v;
     void *out;
     float *lse;
     const int32_t *table, *lens;
-    int *counters;      // workspace: arrivals for the one segment that crosses the end of a CTA's range and
-                        // begins inside it, one count per CTA, zero between calls
-    float *partials;    // workspace: two partial results per CTA
+    int *counters;      // workspace: a segment's groups that have arrived, zero between calls
+    float *partials;    // workspace: the groups' partial results
     int *status;
-    int64_t q_bs, q_hs, o_bs, o_hs;                        // elements
+    int64_t q_bs, q_hs, o_bs, o_hs;                             // elements
     int64_t table_stride, page_stride, slot_stride, head_stride;
-    int B, G, Hkv, D, rows, row_tiles, page, num_pages, cap;   // cap: rows the table has room for
-    int page_shift;                                        // log2(page), -1 if it is no power of two
-    int one_page, whole;                                   // a tile's keys are in one page: page % TK == 0; and D == DP
-    int min_tiles;                                         // fewest tiles worth a CTA
-    float join_cost;                                       // of a partial result in the last join, in tiles
-    uint32_t split_magic;                                  // cluster kernel: ceil(2^32 / CTAs per segment)
-    int stages;                                            // cluster kernel: of each warp's ring
+    int G, Hkv, D, rows, row_tiles, page, num_pages, cap;       // cap: rows the table has room for
+    int one_page, whole;   // a tile's keys are in one page: page % TK == 0; and D == DP
+    int split, groups, stages;
+    Div by_page, by_split, by_groups;
     float scale;
 };
 
@@ -70,14 +80,13 @@ template <typename T_, int DP_, int ROWS_>
 struct Cfg {
     using T = T_;
     static constexpr bool F16 = std::is_same<T, half>::value;
-    static constexpr int DP = DP_, ROWS = ROWS_, STAGES = 2;
+    static constexpr int DP = DP_, ROWS = ROWS_;
     static constexpr int TK = (F16 ? 16 : 8) * (DP <= 64 ? 2 : 1);   // keys per tile
     static constexpr int NCH = DP * (int)sizeof(T) / 16;             // 16-byte chunks per row
     static constexpr int ROW_BYTES = DP * (int)sizeof(T);
     static constexpr int TILE_BYTES = TK * ROW_BYTES;
     static __device__ __forceinline__ uint32_t at(int row, int chunk) { return row * ROW_BYTES + (chunk ^ (row & 7)) * 16; }
-    static constexpr int kWarpsMost = DP > 128 ? 6 : kMaxWarps;      // as far as shared memory goes
-    static constexpr int kCtas = DP > 128 ? 1 : !F16 && ROWS > 4 ? 2 : kMaxCtas;                          // CTAs on an SM, as far as registers go
+    static constexpr int kWarpsMost = DP > 128 ? 6 : kMaxWarps;      // on an SM, two stages each in shared memory
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
@@ -120,50 +129,6 @@ __device__ __forceinline__ void fma4(float4 &c, float s, float4 v) {
     c.x = fmaf(s, v.x, c.x), c.y = fmaf(s, v.y, c.y), c.z = fmaf(s, v.z, c.z), c.w = fmaf(s, v.w, c.w);
 }
 
-// A position in the list of tiles (32 bits: the host refuses longer lists).
-struct Cursor {
-    int b, seg;              // request, segment in it
-    uint32_t tile, tiles;    // tile in the segment, tiles per segment of b
-};
-
-struct Shared {
-    const uint32_t *prefix;    // [B + 1] tiles (of one segment) before request b
-    int B, NS;                 // NS = segments per request
-};
-
-__device__ __forceinline__ Cursor cursor_at(const Shared &sh, uint32_t t) {
-    Cursor c;
-    const uint32_t u = t / (uint32_t)sh.NS;   // among the requests' tiles of one segment each
-    int lo = 0, hi = sh.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (sh.prefix[mid + 1] > u)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
-    c.b = lo;
-    c.tiles = sh.prefix[lo + 1] - sh.prefix[lo];
-    const uint32_t r = t - sh.prefix[lo] * (uint32_t)sh.NS;
-    c.seg = (int)(r / c.tiles);
-    c.tile = r - (uint32_t)c.seg * c.tiles;
-    return c;
-}
-
-// The next tile; the caller knows that there is one.
-__device__ __forceinline__ void advance(const Shared &sh, Cursor &c) {
-    if (++c.tile < c.tiles)
-        return;
-    c.tile = 0;
-    if (++c.seg < sh.NS)
-        return;
-    c.seg = 0;
-    do {
-        c.b++;
-        c.tiles = sh.prefix[c.b + 1] - sh.prefix[c.b];
-    } while (c.tiles == 0);
-}
-
 // Two neighbouring outputs of one row; c is even and below D (a multiple of 8).
 __device__ __forceinline__ void store2(half *p, float a, float b) { *reinterpret_cast<half2 *>(p) = __floats2half2_rn(a, b); }
 __device__ __forceinline__ void store2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
@@ -202,8 +167,8 @@ struct Acc<C, true> {
     float m[NT][2], l[NT][2];
     uint32_t q[KS][NT][2];     // B fragments of the segment's query rows
 
-    // The segment's query rows, just landed at `qs`.
-    __device__ __forceinline__ void open(uint32_t qs, uint32_t, int rows) {
+    // The segment's query rows are at `qs`.
+    __device__ __forceinline__ void open(uint32_t qs, int rows) {
         const int lane = threadIdx.x & 31, i = lane >> 3;
         if constexpr (NT == 1) {
             const int r = min(lane & 7, rows - 1);
@@ -343,30 +308,6 @@ struct Acc<C, true> {
                 }
             }
     }
-
-    // The finished rows: row(r) is the query head of row r, or -1.
-    template <typename F>
-    __device__ __forceinline__ void to_out(half *out, int64_t hs, float *lse, int D, F row) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t2 = (lane & 3) * 2;
-#pragma unroll
-        for (int t = 0; t < NT; t++) {
-            const float i0 = l[t][0] > 0.0f ? 1.0f / l[t][0] : 0.0f, i1 = l[t][1] > 0.0f ? 1.0f / l[t][1] : 0.0f;
-            const int head = row(t * 8 + g);
-            half *p = out + head * hs + t2;
-#pragma unroll
-            for (int k = 0; k < 2 * KS; k++) {
-                const int h = 2 * (k & 1);
-                const uint32_t v = transpose8(h2_as_u32(__floats2half2_rn(o[k / 2][t][h] * i0, o[k / 2][t][h + 1] * i1)));
-                if (head >= 0 && k * 8 < D)
-                    *reinterpret_cast<uint32_t *>(p + k * 8) = v;
-            }
-            if (lse && g < 2) {
-                const int hl = row(t * 8 + t2 + g);
-                if (hl >= 0)
-                    lse[hl] = lse_of(g ? m[t][1] : m[t][0], (g ? l[t][1] : l[t][0]) * kSumScale);
-            }
-        }
-    }
 };
 
 // fp32: every product and sum in fp32 on the CUDA cores, eight keys at a time.
@@ -382,15 +323,7 @@ struct Acc<C, false> {
     float4 o[C::ROWS][PER];
     float m[C::ROWS], l[C::ROWS];
 
-    // The segment's query rows, just landed at `land`: kept at `qs` (which may be `land`).
-    __device__ __forceinline__ void open(uint32_t land, uint32_t qs, int rows) {
-        __syncwarp();   // the last segment's rows have been read
-        for (int i = threadIdx.x & 31; land != qs && i < rows * C::NCH; i += 32) {
-            const float4 v = lds4(land + i * 16);
-            asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(qs + i * 16), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                         : "memory");
-        }
-        __syncwarp();
+    __device__ __forceinline__ void open(uint32_t, int) {
 #pragma unroll
         for (int r = 0; r < C::ROWS; r++) {
 #pragma unroll
@@ -501,25 +434,6 @@ struct Acc<C, false> {
             }
         }
     }
-
-    template <typename F>
-    __device__ __forceinline__ void to_out(float *out, int64_t hs, float *lse, int D, F row) {
-        const int lane = threadIdx.x & 31, col = lane % LPR;
-#pragma unroll
-        for (int r = 0; r < C::ROWS; r++) {
-            const int head = row(r);
-            if (head < 0)
-                continue;
-            const float inv = l[r] > 0.0f ? 1.0f / l[r] : 0.0f;
-#pragma unroll
-            for (int c = 0; c < PER; c++)
-                if (lane < LPR && (col + c * 32) * 4 < D)
-                    *reinterpret_cast<float4 *>(out + head * hs + (col + c * 32) * 4) =
-                        make_float4(o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv);
-            if (lane == 0 && lse)
-                lse[head] = lse_of(m[r], l[r]);
-        }
-    }
 };
 
 // A warp's copies into its ring: lane i holds the table entry of key i of the
@@ -545,7 +459,7 @@ struct Feed {
         ent = -1;
         if (p.one_page || lane < n) {
             const int key = p.one_page ? key0 : key0 + lane;
-            const int blk = p.page_shift >= 0 ? key >> p.page_shift : key / p.page;
+            const int blk = quotient(key, p.by_page);
             ent_off = key - blk * p.page;
             ent = row[blk];
         }
@@ -597,34 +511,11 @@ struct Feed {
         }
         return valid;
     }
-
-    // Starts the copies of a segment's query rows into a stage; head(r) is row r's query head, or -1.
-    template <typename F>
-    __device__ __forceinline__ void query(int stage, int b, F head) {
-        const uint32_t qs = ring + stage * 2 * C::TILE_BYTES;
-        for (int i = threadIdx.x & 31; i < p.rows * C::NCH; i += 32) {
-            const int r = i / C::NCH, ch = i % C::NCH, h = head(r);
-            const bool in = h >= 0 && ch * EPC < p.D;
-            const T *src = (const T *)p.q + (in ? b * p.q_bs + h * p.q_hs + ch * EPC : 0);
-            cp_async16(qs + C::at(r, ch), src, in ? 16 : 0);
-        }
-    }
 };
 
 // A partial result in memory: rows x D outputs, then rows maxima, then rows sums
 // (relative to the maximum, as o is), to a multiple of 16 bytes.
 __host__ __device__ __forceinline__ int partial_floats(int rows, int D) { return (rows * (D + 2) + 3) / 4 * 4; }
-
-// First tile of the i-th of n equal ranges of `total` tiles.
-__device__ __forceinline__ uint32_t range_at(uint32_t total, uint32_t n, uint32_t i) {
-    const uint32_t q = total / n;
-    return q * i + min(i, total - q * n);
-}
-// The range that holds tile t (0 <= t < total).
-__device__ __forceinline__ uint32_t range_of(uint32_t total, uint32_t n, uint32_t t) {
-    const uint32_t q = total / n, r = total - q * n, cut = r * (q + 1);
-    return t < cut ? t / (q + 1) : r + (t - cut) / q;
-}
 
 // Counts an arrival: what the CTA has written is visible to the CTA that counts
 // the last one (called by one thread, behind a barrier of its CTA).
@@ -632,357 +523,6 @@ __device__ __forceinline__ uint32_t arrive(int *counter) {
     uint32_t n;
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(n) : "l"(counter) : "memory");
     return n;
-}
-
-// A segment that more than one warp or CTA works on, as one CTA sees it.
-struct Chain {
-    int warp, parts;         // its first warp here and the number of warps; parts = 0: none
-    int b, seg;
-    uint32_t first, end;     // its tiles in the list
-};
-
-template <typename C>
-__global__ void __launch_bounds__(kThreads, C::kCtas) paged_attention_kernel(const __grid_constant__ AttnParams p) {
-    using T = typename C::T;
-    using A = Acc<C, C::F16>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kRing = C::STAGES * 2 * C::TILE_BYTES;   // bytes a warp
-    uint8_t *ring = smem + (size_t)warp * kRing;
-    const int q_bytes = C::F16 ? 0 : p.rows * C::ROW_BYTES;   // fp32 only: the current query rows
-    const uint32_t q_keep = smem_u32(smem) + kWarps * kRing + warp * q_bytes;
-    const int pf = partial_floats(p.rows, p.D);
-    // a warp's partial results: [0] of the segment that its range begins inside
-    // of, [1] of the one that it opens and does not end, in its drained ring
-    float *heads = reinterpret_cast<float *>(smem + kWarps * (kRing + q_bytes));   // [kWarps][pf]
-    auto slot_of = [&](int w, bool opened) {
-        return opened ? reinterpret_cast<float *>(smem + (size_t)w * kRing) : heads + w * pf;
-    };
-    uint32_t *prefix = reinterpret_cast<uint32_t *>(heads + kWarps * pf);          // [B + 1]
-    __shared__ uint32_t warp_sums[kWarps];
-    __shared__ Chain chains[kWarps + 1];   // [0] the segment that the CTA's range begins inside of, [1 + w] opened by warp w
-    __shared__ int last[2];
-    __shared__ int2 joins[2];
-
-    pdl_wait();
-    pdl_launch_dependents();
-
-    // tiles of each request, and their sums; up to 32 requests: by every warp for itself, to the same words
-    uint32_t carry = 0;
-    bool bad_len = false;
-    const bool alone = p.B <= 32;
-    for (int b0 = 0; b0 < p.B; b0 += alone ? 32 : kThreads) {
-        const int b = b0 + (alone ? lane : (int)threadIdx.x);
-        uint32_t v = 0;
-        if (b < p.B) {
-            const int n = p.lens[b];
-            bad_len |= n < 0 || n > p.cap;
-            v = ((uint32_t)min(max(n, 0), p.cap) + C::TK - 1) / C::TK;
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o)
-                v += u;
-        }
-        if (alone) {
-            carry = __shfl_sync(0xffffffffu, v, 31);
-        } else {
-            __syncthreads();
-            if (lane == 31)
-                warp_sums[warp] = v;
-            __syncthreads();
-            v += carry;
-#pragma unroll
-            for (int w = 0; w < kWarps; w++) {
-                v += w < warp ? warp_sums[w] : 0u;
-                carry += warp_sums[w];
-            }
-        }
-        if (b < p.B)
-            prefix[b + 1] = v;
-    }
-    if (lane == 0)
-        prefix[0] = 0;
-    if (threadIdx.x <= kWarps)
-        chains[threadIdx.x].parts = 0;
-    if (bad_len && blockIdx.x == 0 && p.status)
-        atomicOr(p.status, 2);
-    __syncthreads();
-
-    Shared sh;
-    sh.prefix = prefix, sh.B = p.B, sh.NS = p.Hkv * p.row_tiles;
-    const int Hq = p.Hkv * p.G;
-
-    // requests without a key: zero rows
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-        if (prefix[b + 1] == prefix[b]) {
-            for (int i = threadIdx.x; i < Hq * (p.D / 2); i += kThreads)
-                store2((T *)p.out + b * p.o_bs + (i / (p.D / 2)) * p.o_hs + (i % (p.D / 2)) * 2, 0.0f, 0.0f);
-            if (p.lse)
-                for (int i = threadIdx.x; i < Hq; i += kThreads)
-                    p.lse[(int64_t)b * Hq + i] = -INFINITY;
-        }
-
-    const uint32_t total = carry * (uint32_t)sh.NS;
-    // CTAs at work: at least min_tiles tiles each, and few enough for the joins
-    // (splits of an average segment x join_cost <= tiles of a CTA)
-    const uint32_t least = max((float)p.min_tiles, sqrtf((float)carry / p.B * p.join_cost));
-    const uint32_t nc = min(gridDim.x, max(total / least, 1u));
-    if (blockIdx.x >= nc || total == 0)
-        return;
-    const uint32_t c0 = range_at(total, nc, blockIdx.x), c1 = range_at(total, nc, blockIdx.x + 1);
-    const uint32_t w0 = c0 + range_at(c1 - c0, kWarps, warp), w1 = c0 + range_at(c1 - c0, kWarps, warp + 1);
-    const float scale2 = p.scale * kLog2e;
-
-    // the query head of row r of a segment, or -1 past the group
-    auto head_of = [&](int seg, int r) -> int {
-        if (p.row_tiles == 1)
-            return r < p.G ? seg * p.G + r : -1;   // G = rows
-        const int h = seg / p.row_tiles, i = (seg - h * p.row_tiles) * C::ROWS + r;
-        return r < p.rows && i < p.G ? h * p.G + i : -1;
-    };
-
-    if (w0 < w1) {
-        uint32_t left = w1 - w0, todo = left;     // tiles to issue, tiles to compute
-        Cursor load = cursor_at(sh, w0), cur = load;
-        if (load.tile != 0 && warp == 0 && lane == 0) {
-            const uint32_t end = c0 - load.tile + load.tiles;
-            chains[0] = {0, (int)range_of(c1 - c0, kWarps, min(end, c1) - 1 - c0) + 1, load.b, load.seg, c0 - load.tile, end};
-        }
-        bool load_q = true, cur_q = true;         // the segment's query rows come first
-        int len = min(p.lens[load.b], p.cap);
-        int64_t head_off = (p.row_tiles == 1 ? load.seg : load.seg / p.row_tiles) * p.head_stride;
-        Feed<C> feed(p, smem_u32(ring));
-        auto fetch = [&]() {
-            int n = C::TK;
-            if (load.tile + 1 == load.tiles)
-                n = len - (int)load.tile * C::TK;
-            feed.fetch(p.table + load.b * p.table_stride, (int)load.tile * C::TK, n);
-        };
-        // Starts the copies of the next item (query rows or a tile) into a stage; the tile's valid keys.
-        auto issue = [&](int stage) -> uint32_t {
-            if (load_q) {
-                load_q = false;
-                feed.query(stage, load.b, [&](int r) { return head_of(load.seg, r); });
-                return 0;
-            }
-            const uint32_t valid = feed.tile(stage, head_off);
-            if (--left > 0) {
-                const int b = load.b;
-                advance(sh, load);
-                load_q = load.tile == 0;
-                if (load_q)
-                    head_off = (p.row_tiles == 1 ? load.seg : load.seg / p.row_tiles) * p.head_stride;
-                if (load.b != b)
-                    len = min(p.lens[load.b], p.cap);
-                fetch();
-            }
-            return valid;
-        };
-        A acc;
-        uint32_t vmask[C::STAGES - 1];   // valid keys of the items in flight
-        fetch();
-#pragma unroll
-        for (int s = 0; s < C::STAGES - 1; s++) {
-            vmask[s] = left > 0 ? issue(s) : 0u;
-            cp_commit();
-        }
-        bool opened = cur.tile == 0;   // the segment's first tile is this warp's
-        int stage = 0;
-        while (todo > 0) {
-            __syncwarp();   // every lane has read the stage that the last item left: it takes the next one
-            const int ahead = stage == 0 ? C::STAGES - 1 : stage - 1;
-            const uint32_t nv = left > 0 ? issue(ahead) : 0u;
-            cp_commit();
-            cp_wait<C::STAGES - 1>();
-            __syncwarp();
-            const uint32_t ks = smem_u32(ring) + stage * 2 * C::TILE_BYTES;
-            const uint32_t valid = vmask[0];
-#pragma unroll
-            for (int s = 0; s + 1 < C::STAGES - 1; s++)
-                vmask[s] = vmask[s + 1];
-            vmask[C::STAGES - 2] = nv;
-            stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-            if (cur_q) {
-                cur_q = false;
-                acc.open(ks, q_keep, p.rows);
-                continue;
-            }
-            acc.tile(ks, ks + C::TILE_BYTES, q_keep, p.rows, valid, scale2);
-            todo--;
-            const bool ends = cur.tile + 1 == cur.tiles;
-            if (ends || todo == 0) {
-                acc.finish();
-                if (opened && ends) {
-                    acc.to_out((T *)p.out + cur.b * p.o_bs, p.o_hs, p.lse ? p.lse + (int64_t)cur.b * Hq : nullptr, p.D,
-                               [&](int r) { return head_of(cur.seg, r); });
-                } else {
-                    __syncwarp();   // every lane has read the last tile of a ring that is written over
-                    acc.to_slot(slot_of(warp, opened), p.rows, p.D);
-                    if (opened && lane == 0) {   // and todo == 0: the segment goes on in the next warp
-                        const uint32_t first = w1 - 1 - cur.tile, end = first + cur.tiles;
-                        chains[1 + warp] = {warp, (int)range_of(c1 - c0, kWarps, min(end, c1) - 1 - c0) - warp + 1,
-                                            cur.b, cur.seg, first, end};
-                    }
-                }
-                opened = true;
-                cur_q = true;
-            }
-            if (todo > 0)
-                advance(sh, cur);
-        }
-    }
-    __syncthreads();
-
-    auto write4 = [&](int b, int head, int c, float4 o, float inv) {
-        T *d = (T *)p.out + b * p.o_bs + head * p.o_hs + c;
-        store2(d, o.x * inv, o.y * inv);
-        store2(d + 2, o.z * inv, o.w * inv);
-    };
-
-    // segments that cross warps: finished here, or this CTA's part of them to the workspace; a warp per row
-    bool wrote = false;
-    for (int k = 0; k <= kWarps; k++) {
-        const Chain ch = chains[k];
-        if (ch.parts == 0)
-            continue;
-        const bool whole = ch.first >= c0 && ch.end <= c1;
-        float *dst = p.partials + ((int64_t)blockIdx.x * 2 + (k > 0)) * pf;
-        wrote |= !whole;
-        for (int r = warp; r < p.rows; r += kWarps) {
-            const float *part[kWarps];
-            float w[kWarps], M = -INFINITY, l = 0.0f;
-#pragma unroll
-            for (int j = 0; j < kWarps; j++) {
-                part[j] = slot_of(ch.warp + min(j, ch.parts - 1), k > 0 && j == 0);
-                w[j] = j < ch.parts ? part[j][p.rows * p.D + r] : -INFINITY;
-                M = fmaxf(M, w[j]);
-            }
-            const float base = M == -INFINITY ? 0.0f : M;
-#pragma unroll
-            for (int j = 0; j < kWarps; j++) {
-                w[j] = ex2(w[j] - base);
-                l = fmaf(w[j], part[j][p.rows * p.D + p.rows + r], l);
-            }
-            const int head = whole ? head_of(ch.seg, r) : 0;
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            for (int c = lane * 4; c < p.D; c += 128) {
-                float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < kWarps; j++)
-                    if (j < ch.parts)
-                        fma4(o, w[j], *reinterpret_cast<const float4 *>(part[j] + r * p.D + c));
-                if (!whole)
-                    *reinterpret_cast<float4 *>(dst + r * p.D + c) = o;
-                else if (head >= 0)
-                    write4(ch.b, head, c, o, inv);
-            }
-            if (lane == 0) {
-                if (!whole) {
-                    dst[p.rows * p.D + r] = M;
-                    dst[p.rows * p.D + p.rows + r] = l;
-                } else if (head >= 0 && p.lse) {
-                    p.lse[(int64_t)ch.b * Hq + head] = lse_of(M, l * A::kSumScale);
-                }
-            }
-        }
-    }
-    if (!wrote)   // the same in every thread
-        return;
-
-    // segments that cross CTAs: the CTA that arrives last joins the parts, in CTA order
-    __syncthreads();
-    if (threadIdx.x < 2) {
-        int mine = -1;
-        for (int k = threadIdx.x; k <= (threadIdx.x ? kWarps : 0); k++) {
-            const Chain &ch = chains[k];
-            if (ch.parts == 0 || (ch.first >= c0 && ch.end <= c1))
-                continue;
-            const uint32_t cf = range_of(total, nc, ch.first), cl = range_of(total, nc, ch.end - 1);
-            if (arrive(p.counters + cf) == cl - cf) {
-                p.counters[cf] = 0;
-                mine = k;
-                joins[threadIdx.x] = make_int2((int)cf, (int)(cl - cf) + 1);
-            }
-        }
-        last[threadIdx.x] = mine;
-    }
-    __syncthreads();
-    float *wm = reinterpret_cast<float *>(smem);   // the rings are free now; the host bounds nc so that this fits them
-    for (int kind = 0; kind < 2; kind++) {
-        if (last[kind] < 0)
-            continue;
-        const Chain ch = chains[last[kind]];
-        const int cf = joins[kind].x, np = joins[kind].y;
-        const float *first = p.partials + ((int64_t)cf * 2 + 1) * pf;             // part 0; part i at rest + (i - 1) * 2 pf
-        const float *rest = p.partials + ((int64_t)cf + 1) * 2 * pf;
-        auto part = [&](int i) { return i == 0 ? first : rest + (int64_t)(i - 1) * 2 * pf; };
-        // fewer rows than warps: 2^sh warps share a row and take every 2^sh-th part each
-        const int sh = p.rows == 1 ? 2 : p.rows == 2 ? 1 : 0, sets = 1 << sh;
-        static_assert(kWarps == 4, "sets of warps");
-        float *red = wm + (p.rows * (np + kWarps) + 3) / 4 * 4;                    // [sets][rows][D]
-        for (int r = warp >> sh; r < p.rows; r += kWarps >> sh) {
-            const int set = warp & (sets - 1);
-            float *w = wm + r * (np + kWarps) + set * ((np + sets - 1) >> sh);     // this set's weights
-            // the row's maximum and sum
-            float M = -INFINITY, l = 0.0f;
-            for (int i = lane; i < np; i += 32) {
-                const float mi = __ldcg(part(i) + p.rows * p.D + r), li = __ldcg(part(i) + p.rows * p.D + p.rows + r);
-                const float mn = fmaxf(M, mi), at = mn == -INFINITY ? 0.0f : mn;
-                l = l * ex2(M - at) + li * ex2(mi - at);
-                M = mn;
-                if ((i & (sets - 1)) == set)
-                    w[i >> sh] = mi;
-            }
-            const float mine = M;
-#pragma unroll
-            for (int x = 16; x; x >>= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-            const float base = M == -INFINITY ? 0.0f : M;
-            l *= ex2(mine - base);
-            for (int i = lane; i < np; i += 32)   // the lane's own entries again
-                if ((i & (sets - 1)) == set)
-                    w[i >> sh] = ex2(w[i >> sh] - base);
-#pragma unroll
-            for (int x = 16; x; x >>= 1)
-                l += __shfl_xor_sync(0xffffffffu, l, x);
-            __syncwarp();
-            const int head = head_of(ch.seg, r);
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            for (int c = lane * 4; c < p.D; c += 128) {
-                float4 o = make_float4(0, 0, 0, 0);
-                for (int i0 = set; i0 < np; i0 += 8 * sets) {
-                    float4 v[8];   // eight loads on their way at a time
-#pragma unroll
-                    for (int u = 0; u < 8; u++)
-                        if (i0 + u * sets < np)
-                            v[u] = __ldcg(reinterpret_cast<const float4 *>(part(i0 + u * sets) + r * p.D + c));
-#pragma unroll
-                    for (int u = 0; u < 8; u++)
-                        if (i0 + u * sets < np)
-                            fma4(o, w[(i0 >> sh) + u], v[u]);
-                }
-                if (sets > 1)
-                    *reinterpret_cast<float4 *>(red + (set * p.rows + r) * p.D + c) = o;
-                else if (head >= 0)
-                    write4(ch.b, head, c, o, inv);
-            }
-            if (lane == 0 && set == 0 && head >= 0 && p.lse)
-                p.lse[(int64_t)ch.b * Hq + head] = lse_of(M, l * A::kSumScale);
-            if (sets > 1) {   // one or two rows: every warp is here once
-                __syncthreads();
-                if (set == 0 && head >= 0)
-                    for (int c = lane * 4; c < p.D; c += 128) {
-                        float4 o = make_float4(0, 0, 0, 0);
-                        for (int x = 0; x < sets; x++)
-                            fma4(o, 1.0f, *reinterpret_cast<const float4 *>(red + (x * p.rows + r) * p.D + c));
-                        write4(ch.b, head, c, o, inv);
-                    }
-            }
-        }
-        __syncthreads();
-    }
 }
 
 __device__ __forceinline__ float ld_cluster(uint32_t a) {
@@ -1002,7 +542,6 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
 }
 
 // Waits until at most n (1 .. kMaxStages - 1) groups of this thread's copies are on their way.
-constexpr int kMaxStages = 6;
 __device__ __forceinline__ void cp_wait_rt(int n) {
     switch (n) {
     case 1: cp_wait<1>(); break;
@@ -1013,71 +552,107 @@ __device__ __forceinline__ void cp_wait_rt(int n) {
     }
 }
 
-// The same attention with one cluster of S CTAs per segment: a CTA has an S-th
-// of the segment's tiles, W warps take every W-th of them.  No list, no
-// workspace and no second pass over memory: the parts are joined in shared
-// memory, then through distributed shared memory behind one cluster barrier.
+// Joins up to 32 partial results of a row for four outputs a lane: lane i brings
+// the maximum m and sum l of part i (-inf and 0 behind the last), load(i) the
+// lane's outputs of part i.  Returns the outputs, M and L of the whole.
+template <typename Load>
+__device__ __forceinline__ float4 merge(int parts, float m, float l, float &M, float &L, Load load) {
+    float4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+        if (u < parts)
+            v[u] = load(u);
+    M = m;
+#pragma unroll
+    for (int x = 16; x; x >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    const float w = ex2(m - (M == -INFINITY ? 0.0f : M));
+    L = l * w;
+#pragma unroll
+    for (int x = 16; x; x >>= 1)
+        L += __shfl_xor_sync(0xffffffffu, L, x);
+    float4 o = make_float4(0, 0, 0, 0);
+    for (int i = 0; i < parts; i += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            if (i + u < parts)
+                fma4(o, __shfl_sync(0xffffffffu, w, i + u), v[u]);
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            if (i + 4 + u < parts)
+                v[u] = load(i + 4 + u);
+    }
+    return o;
+}
+
 template <typename C>
-__global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_cluster_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(const __grid_constant__ AttnParams p) {
     using T = typename C::T;
     using A = Acc<C, C::F16>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t vmask[kMaxWarps][kMaxStages];    // valid keys of the tile in each stage
+    __shared__ int last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
     const int kRing = p.stages * 2 * C::TILE_BYTES;   // bytes a warp
     uint8_t *my_ring = smem + (size_t)warp * kRing;
     const uint32_t ring = smem_u32(my_ring);
     uint8_t *q_rows = smem + (size_t)W * kRing;
-    const int rank = blockIdx.x, S = gridDim.x, seg = blockIdx.y, b = blockIdx.z;
+    const int S = p.split, P = p.groups, seg = blockIdx.y, b = blockIdx.z;
+    const int group = P == 1 ? 0 : quotient(blockIdx.x, p.by_split), rank = blockIdx.x - group * S;
     const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, r0 = (seg - h * p.row_tiles) * C::ROWS;
-    auto head_of = [&](int r) { return r0 + r < p.G ? h * p.G + r0 + r : -1; };
+    auto head_of = [&](int r) { return r0 + r < p.G ? h * p.G + r0 + r : -1; };   // of row r of the segment
 
     pdl_wait();
     pdl_launch_dependents();
     const int given = p.lens[b], len = min(max(given, 0), p.cap);
-    if (given != len && rank == 0 && seg == 0 && threadIdx.x == 0 && p.status)
+    if (given != len && blockIdx.x == 0 && seg == 0 && threadIdx.x == 0 && p.status)
         atomicOr(p.status, 2);
     const int tiles = (int)(((uint32_t)len + C::TK - 1) / C::TK);
-    const int per = S == 1 ? tiles : (int)__umulhi((uint32_t)(tiles + S - 1), p.split_magic);   // ceil(tiles / S)
-    const int end = min(tiles, (rank + 1) * per);
-    T *out = (T *)p.out + b * p.o_bs;
-    float *lse = p.lse ? p.lse + (int64_t)b * p.Hkv * p.G : nullptr;
+    // the group's tiles [g0, g1), the CTA's [t0, t1)
+    const int per_group = P == 1 ? tiles : quotient(tiles + P - 1, p.by_groups);
+    const int g0 = group * per_group, g1 = min(tiles, g0 + per_group);
+    if (group > 0 && g0 >= tiles)
+        return;
+    const int used_groups = P == 1 || tiles == 0 ? 1 : (tiles + per_group - 1) / per_group;
+    const int per = S == 1 ? g1 - g0 : quotient(g1 - g0 + S - 1, p.by_split);
+    const int t0 = g0 + rank * per, t1 = min(g1, t0 + per);
 
     const int32_t *row = p.table + b * p.table_stride;
     const int64_t head_off = h * p.head_stride;
-    int t = rank * per + warp, load = t;   // tile to compute, tile to issue
+    int t = t0 + warp, load = t;   // tile to compute, tile to issue
     Feed<C> feed(p, ring);
     auto issue = [&](int stage) {
-        if (load < end) {
+        if (load < t1) {
             const uint32_t valid = feed.tile(stage, head_off);
             if (lane == 0)
                 vmask[warp][stage] = valid;
             load += W;
-            if (load < end)
+            if (load < t1)
                 feed.fetch(row, load * C::TK, min(C::TK, len - load * C::TK));
         }
         cp_commit();
     };
-    if (load < end)
+    if (load < t1)
         feed.fetch(row, load * C::TK, min(C::TK, len - load * C::TK));
     for (int s = 0; s + 1 < p.stages; s++)
         issue(s);
     // the segment's query rows, for all warps
     for (int i = threadIdx.x; i < p.rows * C::NCH; i += blockDim.x) {
-        const int r = i / C::NCH, ch = i % C::NCH, head = head_of(r);
+        const int r = i / C::NCH, ch = i % C::NCH, head = head_of(r), e = ch * (16 / (int)sizeof(T));
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (head >= 0 && ch * (16 / (int)sizeof(T)) < p.D)
-            v = ldg_v4((const T *)p.q + b * p.q_bs + head * p.q_hs + ch * (16 / (int)sizeof(T)));
+        if (head >= 0 && e < p.D)
+            v = ldg_v4((const T *)p.q + b * p.q_bs + head * p.q_hs + e);
         *reinterpret_cast<uint4 *>(q_rows + C::at(r, ch)) = v;
     }
     __syncthreads();
 
-    A acc;
-    if (t < end) {
+    const int part_at = p.rows * p.D;   // of a partial result's maxima; the sums follow
+    if (t < t1) {
+        A acc;
         const uint32_t qs = smem_u32(q_rows);
-        acc.open(qs, qs, p.rows);
+        acc.open(qs, p.rows);
         int stage = 0;
-        for (; t < end; t += W) {
+        for (; t < t1; t += W) {
             __syncwarp();   // every lane has read the stage that the last tile left: it takes the next one
             issue(stage == 0 ? p.stages - 1 : stage - 1);
             cp_wait_rt(p.stages - 1);
@@ -1087,184 +662,173 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_cluster_ke
             stage = stage + 1 == p.stages ? 0 : stage + 1;
         }
         acc.finish();
-        __syncwarp();
+        __syncwarp();   // every lane has read the last tile of a ring that is written over
         acc.to_slot(reinterpret_cast<float *>(my_ring), p.rows, p.D);
     }
     __syncthreads();
 
-    // The CTA's warps joined: a warp per row and 128 outputs, lane i looks after warp i.
+    // The joins: a warp per row and 128 outputs.
     const int chunks = (p.D + 127) >> 7, tasks = p.rows * chunks;
-    const int parts = min(max(end - rank * per, 0), W);
-    float *cta_part = reinterpret_cast<float *>(smem) + partial_floats(p.rows, p.D);   // in warp 0's ring, behind its part
-    for (int task = warp; task < tasks; task += W) {
-        const int r = chunks == 1 ? task : task >> 1, c = (chunks == 1 ? 0 : (task & 1) * 128) + lane * 4;
-        const float *ml = reinterpret_cast<const float *>(smem + (size_t)lane * kRing) + p.rows * p.D + r;
-        const float m = lane < parts ? ml[0] : -INFINITY;
-        float l = lane < parts ? ml[p.rows] : 0.0f, M = m;
-#pragma unroll
-        for (int x = 16; x; x >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        const float w = ex2(m - (M == -INFINITY ? 0.0f : M));
-        l *= w;
-#pragma unroll
-        for (int x = 16; x; x >>= 1)
-            l += __shfl_xor_sync(0xffffffffu, l, x);
-        float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-        for (int i = 0; i < parts; i++) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            if (c < p.D)
-                fma4(o, wi, *reinterpret_cast<const float4 *>(smem + (size_t)i * kRing + (r * p.D + c) * 4));
+    const int pf = partial_floats(p.rows, p.D), id = b * gridDim.y + seg;
+    auto row_of = [&](int task) { return chunks == 1 ? task : task >> 1; };
+    auto col_of = [&](int task) { return (chunks == 1 ? 0 : (task & 1) * 128) + lane * 4; };
+    auto keep = [&](float *part, int r, int c, float4 o, float M, float L) {
+        if (c < p.D)
+            *reinterpret_cast<float4 *>(part + r * p.D + c) = o;
+        if (c == 0)
+            part[part_at + r] = M, part[part_at + p.rows + r] = L;
+    };
+    auto write = [&](int r, int c, float4 o, float M, float L) {
+        const int head = head_of(r);
+        if (head < 0)
+            return;
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        if (c < p.D) {
+            T *d = (T *)p.out + b * p.o_bs + head * p.o_hs + c;
+            store2(d, o.x * inv, o.y * inv);
+            store2(d + 2, o.z * inv, o.w * inv);
         }
-        if (S > 1) {
-            if (c < p.D)
-                *reinterpret_cast<float4 *>(cta_part + r * p.D + c) = o;
-            if (c == 0) {
-                cta_part[p.rows * p.D + r] = M;
-                cta_part[p.rows * p.D + p.rows + r] = l;
-            }
-        } else {
-            const int head = head_of(r);
-            if (head >= 0) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                if (c < p.D) {
-                    T *d = out + head * p.o_hs + c;
-                    store2(d, o.x * inv, o.y * inv);
-                    store2(d + 2, o.z * inv, o.w * inv);
-                }
-                if (c == 0 && lse)
-                    lse[head] = lse_of(M, l * A::kSumScale);
-            }
+        if (c == 0 && p.lse)
+            p.lse[(int64_t)b * p.Hkv * p.G + head] = lse_of(M, L * A::kSumScale);
+    };
+    float *group_part = p.partials + ((int64_t)id * P + group) * pf;
+
+    // of the CTA's warps
+    float *cta_part = reinterpret_cast<float *>(smem) + pf;   // in warp 0's ring, behind its part
+    {
+        const int parts = min(max(t1 - t0, 0), W);
+        for (int task = warp; task < tasks; task += W) {
+            const int r = row_of(task), c = col_of(task);
+            const float *ml = reinterpret_cast<const float *>(smem + (size_t)lane * kRing) + part_at + r;
+            float M, L;
+            const float4 o = merge(parts, lane < parts ? ml[0] : -INFINITY, lane < parts ? ml[p.rows] : 0.0f, M, L, [&](int i) {
+                return *reinterpret_cast<const float4 *>(smem + (size_t)i * kRing + (r * p.D + (c < p.D ? c : 0)) * 4);
+            });
+            if (S > 1)
+                keep(cta_part, r, c, o, M, L);
+            else if (used_groups > 1)
+                keep(group_part, r, c, o, M, L);
+            else
+                write(r, c, o, M, L);
         }
     }
+    // of the cluster's CTAs
     if (S > 1) {
         cluster_sync();
-        // the ranks joined, the same way; lane i looks after rank i
-        const int used = per > 0 ? (tiles + per - 1) / per : 0;   // ranks with a tile
-        const uint32_t mine = cluster_map(smem_u32(cta_part), lane < used ? lane : rank);
+        const int parts = per > 0 ? (g1 - g0 + per - 1) / per : 0;   // CTAs with a tile
+        const uint32_t at = smem_u32(cta_part);
         for (int task = warp * S + rank; task < tasks; task += W * S) {
-            const int r = chunks == 1 ? task : task >> 1, c = (chunks == 1 ? 0 : (task & 1) * 128) + lane * 4;
-            const uint32_t ml = mine + (p.rows * p.D + r) * 4;
-            const float m = lane < used ? ld_cluster(ml) : -INFINITY;
-            float l = lane < used ? ld_cluster(ml + p.rows * 4) : 0.0f, M = m;
-            float4 v[8];
-            const uint32_t at = (r * p.D + (c < p.D ? c : 0)) * 4;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const uint32_t part = __shfl_sync(0xffffffffu, mine, i);
-                v[i] = i < used ? ld_cluster4(part + at) : make_float4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int x = 16; x; x >>= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-            const float w = ex2(m - (M == -INFINITY ? 0.0f : M));
-            l *= w;
-#pragma unroll
-            for (int x = 16; x; x >>= 1)
-                l += __shfl_xor_sync(0xffffffffu, l, x);
-            float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                fma4(o, __shfl_sync(0xffffffffu, w, i), v[i]);
-            for (int i = 8; i < used; i++)
-                fma4(o, __shfl_sync(0xffffffffu, w, i), ld_cluster4(__shfl_sync(0xffffffffu, mine, i) + at));
-            const int head = head_of(r);
-            if (head >= 0) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                if (c < p.D) {
-                    T *d = out + head * p.o_hs + c;
-                    store2(d, o.x * inv, o.y * inv);
-                    store2(d + 2, o.z * inv, o.w * inv);
-                }
-                if (c == 0 && lse)
-                    lse[head] = lse_of(M, l * A::kSumScale);
-            }
+            const int r = row_of(task), c = col_of(task);
+            const uint32_t ml = cluster_map(at + (part_at + r) * 4, lane < parts ? lane : rank);
+            const float m = lane < parts ? ld_cluster(ml) : -INFINITY, l = lane < parts ? ld_cluster(ml + p.rows * 4) : 0.0f;
+            float M, L;
+            const float4 o = merge(parts, m, l, M, L, [&](int i) {
+                return ld_cluster4(cluster_map(at + (r * p.D + (c < p.D ? c : 0)) * 4, i));
+            });
+            if (used_groups > 1)
+                keep(group_part, r, c, o, M, L);
+            else
+                write(r, c, o, M, L);
         }
+        if (used_groups > 1)
+            __threadfence();
         cluster_sync();   // no CTA leaves while another reads its part
+    }
+    // of the segment's groups
+    if (used_groups > 1 && rank == 0) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            last = arrive(p.counters + id) == (uint32_t)used_groups - 1;
+            if (last)
+                p.counters[id] = 0;
+        }
+        __syncthreads();
+        if (!last)
+            return;
+        const float *first = p.partials + (int64_t)id * P * pf;
+        for (int task = warp; task < tasks; task += W) {
+            const int r = row_of(task), c = col_of(task);
+            float m = -INFINITY, l = 0.0f, M, L;
+            if (lane < used_groups) {
+                m = __ldcg(first + (int64_t)lane * pf + part_at + r);
+                l = __ldcg(first + (int64_t)lane * pf + part_at + p.rows + r);
+            }
+            const float4 o = merge(used_groups, m, l, M, L, [&](int i) {
+                return __ldcg(reinterpret_cast<const float4 *>(first + (int64_t)i * pf + r * p.D + (c < p.D ? c : 0)));
+            });
+            write(r, c, o, M, L);
+        }
     }
 }
 
 constexpr size_t kSmemMax = 227 * 1024 - 256;
 constexpr size_t kSmemSm = 228 * 1024;
 
-// Tuning hook: 0 = the rule in launch_cfg, 1 = always the list, 2 = always clusters.
-int g_mode = 0, g_split = 0, g_warps = 0;
+// Tuning hook: what is not 0 replaces the rule's choice.
+int g_split = 0, g_warps = 0, g_groups = 0;
 
 template <typename C>
-int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
-    static int caches[2][kMaxDevices] = {};
-    const int segs = p.Hkv * p.row_tiles;
+int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
+    static int cache[kMaxDevices] = {};
+    const int segs = p.Hkv * p.row_tiles, sms = device_sm_count();
+    const int64_t all = (int64_t)B * segs;
+    const int tiles = (p.cap - 1) / C::TK + 1;   // of the longest request that the table has room for
     p.one_page = p.page % C::TK == 0;
     p.whole = p.one_page && p.D == C::DP;
-    p.page_shift = (p.page & (p.page - 1)) == 0 ? __builtin_ctz((unsigned)p.page) : -1;
-    const int64_t most_tiles = (p.cap - 1) / C::TK + 1, tiles = most_tiles * p.B * segs;
-    if (tiles > 0x7fffffff)
-        return fail(MNB_ERR_SHAPE, "mnb_paged_attention: B=%d requests of up to %d tokens in %d heads are 2^31 tiles or more",
-                    p.B, p.cap, segs);
-    const size_t ring = (size_t)kWarps * (C::STAGES * 2 * C::TILE_BYTES + (C::F16 ? 0 : p.rows * C::ROW_BYTES));
-    const size_t list = ring + (size_t)kWarps * partial_floats(p.rows, p.D) * 4 + (size_t)(p.B + 1) * 4;
-    if (list > kSmemMax)
-        return fail(MNB_ERR_UNSUPPORTED, "mnb_paged_attention: %zu bytes of shared memory needed", list);
-    auto resident = [&](size_t smem) {
-        const int fit = (int)(kSmemSm / (smem + 1024 + 512));
-        return device_sm_count() * (fit < C::kCtas ? fit : C::kCtas);
-    };
-
-    // Clusters.
-    const int64_t all = (int64_t)p.B * segs;
-    const size_t per_warp = (size_t)C::TILE_BYTES * 2, q_bytes = (size_t)p.rows * C::ROW_BYTES;
-    int split = (int)(resident(kWarps * 2 * per_warp + q_bytes) / all < 8 ? resident(kWarps * 2 * per_warp + q_bytes) / all : 8);
-    const int64_t by_tiles = (most_tiles - 1) / kWarps + 1;
-    split = split < by_tiles ? split : (int)by_tiles;
-    split = g_split ? g_split : split < 1 ? 1 : split;
-    int warps = g_warps ? g_warps : kWarps;
-    const int fit_warps = (int)((kSmemMax - q_bytes) / (2 * per_warp));
-    warps = warps < fit_warps ? warps : fit_warps;
-    warps = warps < C::kWarpsMost ? warps : C::kWarpsMost;
-    p.split_magic = split > 1 ? (uint32_t)((((uint64_t)1 << 32) + split - 1) / split) : 0;
-    const int64_t warp_tiles = (most_tiles - 1) / (warps * split) + 1;
-    const bool clusters = g_mode == 2 || (g_mode == 0 && warp_tiles <= kClusterTiles);
+    // An SM has room for kWarpsMost warps' rings: as one CTA while clusters of 8 of
+    // them, one per segment, leave SMs idle, else as two or three.
+    const int ctas_sm = all * 9 <= sms ? 1 : all * 9 <= 2 * sms ? 2 : 3;
+    int warps = C::kWarpsMost / ctas_sm;
+    int64_t split = (int64_t)ctas_sm * sms / all;
+    if (ctas_sm == 3) {   // more CTAs only for work: 4 tiles a warp or more, and not far beyond 32
+        const int64_t most = (tiles - 1) / (warps * 4) + 1, least = (tiles - 1) / (warps * 32) + 1;
+        split = split < most ? split : most;
+        split = split > least ? split : least;
+    }
+    split = split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split;
+    split = split < tiles ? split : tiles;
+    split = g_split ? g_split : split;
+    warps = (tiles - 1) / (int)split + 1 < warps ? (tiles - 1) / (int)split + 1 : warps;
+    warps = g_warps ? g_warps < C::kWarpsMost ? g_warps : C::kWarpsMost : warps;
+    // Groups: where the clusters of a few long segments would leave SMs idle, until a warp has 4 tiles.
+    int64_t groups = 1;
+    if (ctas_sm == 1 && tiles > 6 * split * warps) {
+        const int64_t want = (tiles - 1) / (4 * split * warps) + 1, room = sms / (9 * all);
+        groups = want < room ? want : room;
+    }
+    groups = g_groups ? g_groups : groups;
+    groups = groups < 32 ? groups : 32;
+    groups = all * groups > kMaxGroups || groups < 1 ? 1 : groups;
+    // A deeper ring where the CTAs leave room for one.
+    const size_t stage = (size_t)warps * 2 * C::TILE_BYTES, q_bytes = (size_t)p.rows * C::ROW_BYTES;
+    const int64_t ctas = all * split * groups, most_sm = C::kWarpsMost / warps;
+    const int64_t per_sm = (ctas - 1) / sms + 1 < most_sm ? (ctas - 1) / sms + 1 : most_sm;
+    size_t room = kSmemSm / per_sm - 1024 - 512;
+    room = room < kSmemMax ? room : kSmemMax;
+    const size_t fit = (room - q_bytes) / stage;
+    p.stages = fit < 2 ? 2 : fit > kMaxStages ? kMaxStages : (int)fit;
+    p.split = (int)split, p.groups = (int)groups;
+    p.by_page = div_by((uint32_t)p.page), p.by_split = div_by((uint32_t)split), p.by_groups = div_by((uint32_t)groups);
 
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)(split * groups), (unsigned)segs, (unsigned)B);
+    cfg.blockDim = dim3((unsigned)warps * 32);
+    cfg.dynamicSmemBytes = p.stages * stage + q_bytes;
     cfg.stream = s;
     cfg.attrs = attr;
-    if (clusters) {
-        // a deeper ring where the SMs have room for one
-        const int64_t ctas = all * split, sms = device_sm_count();
-        const int most_ctas = kMaxWarps / warps;
-        const int per_sm = ctas > sms * (most_ctas - 1) ? most_ctas : (int)((ctas - 1) / sms) + 1;
-        const size_t room = kSmemSm / per_sm - 1024 - 1024;
-        const size_t fit = ((room < kSmemMax ? room : kSmemMax) - q_bytes) / (warps * per_warp);
-        p.stages = fit < 2 ? 2 : fit > kMaxStages ? kMaxStages : (int)fit;
-        cfg.blockDim = dim3((unsigned)warps * 32);
-        cfg.gridDim = dim3((unsigned)split, (unsigned)segs, (unsigned)p.B);
-        cfg.dynamicSmemBytes = p.stages * warps * per_warp + q_bytes;
-        if (split > 1) {
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = (unsigned)split;
-            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-            cfg.numAttrs = 1;
-        }
-    } else {
-        // CTAs worth the table's width; the last join keeps a float per row and part, and an output row per warp,
-        // in the rings
-        const int64_t want = (tiles - 1) / p.min_tiles + 1;
-        const int joinable = (kWarps * (C::STAGES * 2 * C::TILE_BYTES - p.D * 4) - 32) / (4 * p.rows) - kWarps;
-        int grid = resident(list);
-        grid = grid < joinable ? grid : joinable;
-        cfg.gridDim = dim3((unsigned)(want < grid ? want : grid));
-        cfg.dynamicSmemBytes = list;
+    if (split > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)split;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
     }
     if (flags & MNB_FLAG_PDL) {
         attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
-    auto *kernel = clusters ? paged_attention_cluster_kernel<C> : paged_attention_kernel<C>;
-    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)cfg.dynamicSmemBytes, caches[clusters]);
-    if (e == cudaSuccess && clusters && split > 8)
-        e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    auto *kernel = paged_attention_kernel<C>;
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), (int)cfg.dynamicSmemBytes, cache);
     if (e == cudaSuccess)
         e = cudaLaunchKernelEx(&cfg, kernel, p);
     if (e != cudaSuccess)
@@ -1273,36 +837,35 @@ int launch_cfg(AttnParams p, unsigned flags, cudaStream_t s) {
 }
 
 template <typename T, int DP, int ROWS>
-int launch_rows(const AttnParams &p, unsigned flags, cudaStream_t s) {
-    return launch_cfg<Cfg<T, DP, ROWS>>(p, flags, s);
+int launch_rows(const AttnParams &p, int B, unsigned flags, cudaStream_t s) {
+    return launch_cfg<Cfg<T, DP, ROWS>>(p, B, flags, s);
 }
 
 template <typename T, int DP>
-int launch_dp(const AttnParams &p, unsigned flags, cudaStream_t s) {
+int launch_dp(const AttnParams &p, int B, unsigned flags, cudaStream_t s) {
     if constexpr (std::is_same<T, half>::value)
-        return p.rows > 8 ? launch_rows<T, DP, 16>(p, flags, s) : launch_rows<T, DP, 8>(p, flags, s);
+        return p.rows > 8 ? launch_rows<T, DP, 16>(p, B, flags, s) : launch_rows<T, DP, 8>(p, B, flags, s);
     else
-        return p.rows > 4   ? launch_rows<T, DP, 8>(p, flags, s)
-               : p.rows > 2 ? launch_rows<T, DP, 4>(p, flags, s)
-               : p.rows > 1 ? launch_rows<T, DP, 2>(p, flags, s)
-                            : launch_rows<T, DP, 1>(p, flags, s);
+        return p.rows > 4   ? launch_rows<T, DP, 8>(p, B, flags, s)
+               : p.rows > 2 ? launch_rows<T, DP, 4>(p, B, flags, s)
+               : p.rows > 1 ? launch_rows<T, DP, 2>(p, B, flags, s)
+                            : launch_rows<T, DP, 1>(p, B, flags, s);
 }
 
 int rows_per_segment(int G, int f16) { return G < (f16 ? 16 : 8) ? G : (f16 ? 16 : 8); }
-int grid_of() { return device_sm_count() * kMaxCtas; }
-size_t counters_bytes() { return ((size_t)grid_of() * 4 + 127) / 128 * 128; }
+constexpr size_t kCounterBytes = kMaxGroups * 4;
 
 }  // namespace
 
-int set_paged_attention_mode(int mode, int split, int warps) {
-    if (mode < 0 || mode > 2 || split < 0 || split > 16 || warps < 0 || warps > kMaxWarps)
+int set_paged_attention_shape(int split, int warps, int groups) {
+    if (split < 0 || split > kMaxSplit || warps < 0 || warps > kMaxWarps || groups < 0 || groups > 32)
         return MNB_ERR_INVALID_ARG;
-    g_mode = mode, g_split = split, g_warps = warps;
+    g_split = split, g_warps = warps, g_groups = groups;
     return MNB_OK;
 }
 
 size_t paged_attention_workspace_bytes(int Hq, int Hkv, int D, int f16) {
-    return counters_bytes() + (size_t)grid_of() * 2 * partial_floats(rows_per_segment(Hq / Hkv, f16), D) * 4;
+    return kCounterBytes + (size_t)kMaxGroups * partial_floats(rows_per_segment(Hq / Hkv, f16), D) * 4;
 }
 
 int launch_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_paged_cache *c, const int32_t *table,
@@ -1314,25 +877,23 @@ int launch_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_
     p.q = q, p.k = c->k, p.v = c->v, p.out = out, p.lse = lse, p.table = table, p.lens = lens, p.status = status;
     p.q_bs = q_bs, p.q_hs = q_hs, p.o_bs = o_bs, p.o_hs = o_hs, p.table_stride = table_stride;
     p.page_stride = c->page_stride, p.slot_stride = c->slot_stride, p.head_stride = c->head_stride;
-    p.B = B, p.Hkv = (int)c->num_heads, p.G = Hq / p.Hkv, p.D = (int)c->head_dim;
+    p.Hkv = (int)c->num_heads, p.G = Hq / p.Hkv, p.D = (int)c->head_dim;
     p.rows = rows_per_segment(p.G, f16);
     p.row_tiles = (p.G + p.rows - 1) / p.rows;
     p.page = (int)c->page_size, p.num_pages = (int)c->num_pages, p.cap = max_blocks * p.page, p.scale = scale;
-    p.min_tiles = kWarps;
-    p.join_cost = (float)(p.rows * (p.D + 2) * 4) / (2 * (f16 ? 16 * 2 : 8 * 4) * p.D);   // bytes over bytes
     p.counters = (int *)workspace;
-    p.partials = (float *)((uint8_t *)workspace + counters_bytes());
+    p.partials = (float *)((uint8_t *)workspace + kCounterBytes);
     if (f16)
-        return p.D <= 64    ? launch_dp<half, 64>(p, flags, s)
-               : p.D <= 128 ? launch_dp<half, 128>(p, flags, s)
-                            : launch_dp<half, 256>(p, flags, s);
-    return p.D <= 64    ? launch_dp<float, 64>(p, flags, s)
-           : p.D <= 128 ? launch_dp<float, 128>(p, flags, s)
-                        : launch_dp<float, 256>(p, flags, s);
+        return p.D <= 64    ? launch_dp<half, 64>(p, B, flags, s)
+               : p.D <= 128 ? launch_dp<half, 128>(p, B, flags, s)
+                            : launch_dp<half, 256>(p, B, flags, s);
+    return p.D <= 64    ? launch_dp<float, 64>(p, B, flags, s)
+           : p.D <= 128 ? launch_dp<float, 128>(p, B, flags, s)
+                        : launch_dp<float, 256>(p, B, flags, s);
 }
 
 }  // namespace mnb
 
-extern "C" MNB_API int mnb_tune_paged_attention(int mode, int split, int warps) {
-    return mnb::set_paged_attention_mode(mode, split, warps);
+extern "C" MNB_API int mnb_tune_paged_attention(int split, int warps, int groups) {
+    return mnb::set_paged_attention_shape(split, warps, groups);
 }

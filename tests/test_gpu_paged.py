@@ -197,13 +197,11 @@ def test_append_keys_and_values_alone(mnb, cuda_dev):
 
 # ---------------------------------------------------------------- attention
 
-@pytest.fixture(params=["by_sizes", "list", "1x4", "2x12", "5x3", "8x4"])
-def kernel(mnb, request):
-    """Each test with the kernel that the sizes choose, with the one that cuts a list, and with clusters of
-    (CTAs)x(warps)."""
-    mode = dict(by_sizes=0, list=1).get(request.param, 2)
-    split, warps = map(int, request.param.split("x")) if mode == 2 else (0, 0)
-    assert mnb._lib.mnb_tune_paged_attention(mode, split, warps) == 0
+@pytest.fixture(params=["by sizes", "1x4x1", "2x12x1", "5x3x1", "8x4x1", "3x2x5", "1x5x7", "8x12x2"])
+def shape(mnb, request):
+    """Each test with the launch shape that its sizes choose, and with others: CTAs of a cluster, warps, clusters."""
+    given = [0, 0, 0] if request.param == "by sizes" else map(int, request.param.split("x"))
+    assert mnb._lib.mnb_tune_paged_attention(*given) == 0
     yield request.param
     mnb._lib.mnb_tune_paged_attention(0, 0, 0)
 
@@ -259,7 +257,7 @@ CASES = [
 
 @pytest.mark.parametrize("dtype", [F16, F32])
 @pytest.mark.parametrize("i", range(len(CASES)))
-def test_attention(mnb, cuda_dev, kernel, i, dtype):
+def test_attention(mnb, cuda_dev, shape, i, dtype):
     lens, Hq, H, D, ps, heads_first = CASES[i]
     case = paged_case(i, lens, Hq, H, D, ps, dtype, heads_first)
     scale = D ** -0.5
@@ -268,7 +266,7 @@ def test_attention(mnb, cuda_dev, kernel, i, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F16, F32])
-def test_attention_many_requests(mnb, cuda_dev, kernel, dtype):
+def test_attention_many_requests(mnb, cuda_dev, shape, dtype):
     rng = np.random.default_rng(5)
     case = paged_case(9, rng.integers(0, 9, 4096).tolist(), 2, 1, 64, 4, dtype)
     out, lse = run_attn(mnb, cuda_dev, case, 0.125)
@@ -277,14 +275,14 @@ def test_attention_many_requests(mnb, cuda_dev, kernel, dtype):
 
 @pytest.mark.parametrize("dtype", [F16, F32])
 @pytest.mark.parametrize("scale,q_scale", [(0.0, 1.0), (-0.1, 2.0), (1.0, 8.0), (0.088, 100.0)])
-def test_attention_scales(mnb, cuda_dev, kernel, scale, q_scale, dtype):
+def test_attention_scales(mnb, cuda_dev, shape, scale, q_scale, dtype):
     """No scale at all (the mean of v), a negative one, and scores of hundreds (one key holds nearly all)."""
     case = paged_case(11, [500, 33, 1], 4, 2, 128, 16, dtype, q_scale=q_scale)
     out, lse = run_attn(mnb, cuda_dev, case, scale)
     assert_attn(out, lse, case, scale)
 
 
-def test_attention_small_probabilities_count(mnb, cuda_dev, kernel):
+def test_attention_small_probabilities_count(mnb, cuda_dev, shape):
     """One key of weight 1 and 20000 of weight 2^-20: together 2^-6 of the sum, none lost to fp16's range."""
     n, D = 20001, 64
     q, k, v, table, lens = paged_case(12, [n], 1, 1, D, 16, F16)
@@ -302,7 +300,7 @@ def test_attention_small_probabilities_count(mnb, cuda_dev, kernel):
     assert abs(float(out[0, 0, 0]) - 20000 / (20000 + 2.0 ** 20)) < 2e-4
 
 
-def test_attention_bad_pages_and_lengths(mnb, cuda_dev, kernel):
+def test_attention_bad_pages_and_lengths(mnb, cuda_dev, shape):
     case = paged_case(13, [100, 64, 40, 16], 4, 2, 64, 16, F16)
     q, k, v, table, lens = case
     table[0, 1], table[1, 0], table[3, 0] = -1, 10 ** 9, k.shape[0]     # a request without any page left, too
@@ -322,7 +320,7 @@ def test_attention_bad_pages_and_lengths(mnb, cuda_dev, kernel):
     assert int(st) == 2
 
 
-def test_attention_without_lse_and_strided_views(mnb, cuda_dev, kernel):
+def test_attention_without_lse_and_strided_views(mnb, cuda_dev, shape):
     """q inside a fused product, out inside a wider buffer that stays as it is around it."""
     case = paged_case(15, [100, 257, 3], 4, 2, 128, 16, F16)
     q, k, v, table, lens = case
@@ -357,7 +355,7 @@ def test_attention_one_workspace_for_all_and_same_bits(mnb, cuda_dev):
     assert int(ws[:1024].sum()) == 0
 
 
-def test_attention_offsets_beyond_32_bits(mnb, cuda_dev, kernel):
+def test_attention_offsets_beyond_32_bits(mnb, cuda_dev, shape):
     """Pages more than 2^31 elements into the pool."""
     ps, H, D = 16, 8, 128
     P = (2 ** 31) // (ps * H * D) + 40
