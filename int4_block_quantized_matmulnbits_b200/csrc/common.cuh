@@ -36,6 +36,23 @@ int device_sm_count();
 constexpr int kMaxDevices = 128;
 cudaError_t ensure_dynamic_smem(const void *kernel, int bytes, int *cache);
 
+// Division of a number below 2^31 by an invariant one: Granlund and Montgomery,
+// "Division by Invariant Integers using Multiplication" (1994), figure 4.1.
+struct Div {
+    uint32_t m;
+    int sh1, sh2;
+};
+inline Div div_by(uint32_t d) {
+    int l = 0;
+    while (((uint64_t)1 << l) < d)
+        l++;
+    return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l < 1 ? l : 1, l > 1 ? l - 1 : 0};
+}
+__device__ __forceinline__ int quotient(int n, const Div &d) {
+    const uint32_t t = __umulhi(d.m, (uint32_t)n);
+    return (int)((t + (((uint32_t)n - t) >> d.sh1)) >> d.sh2);
+}
+
 // ---------------------------------------------------------------- device PTX
 
 __device__ __forceinline__ uint32_t lop3_and_or(uint32_t a, uint32_t mask, uint32_t magic) {

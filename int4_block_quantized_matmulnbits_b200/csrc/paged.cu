@@ -9,7 +9,6 @@ namespace {
 
 // ------------------------------------------------------------- paged tables
 
-constexpr int kTabThreads = 512;
 constexpr uint32_t kRefused = 0x80000000u;   // a request's page offset: it was granted nothing
 
 // Sum of counts that stops at 2^31 - 1 (associative for operands below 2^31).
@@ -17,6 +16,7 @@ __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min
 
 // Inclusive saturating scan over the CTA; `total` gets the CTA's sum.  Two
 // barriers; `warp_sums` must not be reused before the next barrier.
+template <int NT>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, uint32_t &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -32,7 +32,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, 
     uint32_t before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kTabThreads / 32; w++) {
+    for (int w = 0; w < NT / 32; w++) {
         const uint32_t s = warp_sums[w];
         if (w < warp)
             before = sat_add(before, s);
@@ -58,18 +58,19 @@ __device__ __forceinline__ int blocks_of(int64_t tokens, int page) { return (int
 // if the request held it before the call and in the free list otherwise, so
 // nothing that this launch writes is read back.  Bound by latency: the lengths'
 // load, the scans and the page's load follow one another.
-__global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const __grid_constant__ TabParams p) {
+template <int NT>
+__global__ void __launch_bounds__(NT) paged_tables_kernel(const __grid_constant__ TabParams p) {
     extern __shared__ uint32_t sh[];
     uint32_t *cu = sh;                    // [B + 1] tokens before request b
     uint32_t *pg = sh + p.B + 1;          // [B] pages taken before request b, kRefused when it gets none
-    __shared__ uint32_t warp_sums[kTabThreads / 32];
+    __shared__ uint32_t warp_sums[NT / 32];
     pdl_wait();
     pdl_launch_dependents();
     const int start = *p.free_start;
     const uint32_t avail = (start >= 0 && start <= p.num_free) ? (uint32_t)(p.num_free - start) : 0u;
     int bad = (start < 0 || start > p.num_free) ? 4 : 0;
     uint32_t tok0 = 0, pg0 = 0, granted = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kTabThreads) {
+    for (int b0 = 0; b0 < p.B; b0 += NT) {
         const int b = b0 + (int)threadIdx.x;
         int c = 0, n = 0, need = 0;
         bool ok = true;
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const __grid_
         }
         const uint32_t cnt = n > 0 ? (uint32_t)n : 0u;
         uint32_t tot;
-        const uint32_t incl = sat_add(block_scan(cnt, warp_sums, tot), tok0);
+        const uint32_t incl = sat_add(block_scan<NT>(cnt, warp_sums, tot), tok0);
         tok0 = sat_add(tok0, tot);
         if (b < p.B) {
             cu[b + 1] = incl;
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const __grid_
             else
                 need = blocks_of(len, p.page) - blocks_of(c, p.page);
         }
-        const uint32_t pincl = sat_add(block_scan((uint32_t)need, warp_sums, tot), pg0);
+        const uint32_t pincl = sat_add(block_scan<NT>((uint32_t)need, warp_sums, tot), pg0);
         pg0 = sat_add(pg0, tot);
         if (b < p.B) {
             // the list runs out at one request; a later one passes only if it needs no page
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const __grid_
             warp_sums[threadIdx.x >> 5] = granted;
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int w = 1; w < kTabThreads / 32; w++)
+            for (int w = 1; w < NT / 32; w++)
                 granted = max(granted, warp_sums[w]);
             *p.free_next = start + (int)granted;
             p.cu[0] = 0;
@@ -126,8 +127,8 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const __grid_
     }
     // requests: one warp each
     const int lane = threadIdx.x & 31;
-    const int warps = gridDim.x * (kTabThreads / 32);
-    for (int b = blockIdx.x * (kTabThreads / 32) + (threadIdx.x >> 5); b < p.B; b += warps) {
+    const int warps = gridDim.x * (NT / 32);
+    for (int b = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); b < p.B; b += warps) {
         const int c = max(p.ctx[b], 0), n = max(p.neu[b], 0);
         const uint32_t first = pg[b];
         const bool ok = first != kRefused;
@@ -142,8 +143,8 @@ __global__ void __launch_bounds__(kTabThreads) paged_tables_kernel(const __grid_
         }
     }
     // tokens: one thread each
-    for (int64_t t64 = (int64_t)blockIdx.x * kTabThreads + threadIdx.x; t64 < p.T;
-         t64 += (int64_t)gridDim.x * kTabThreads) {
+    for (int64_t t64 = (int64_t)blockIdx.x * NT + threadIdx.x; t64 < p.T;
+         t64 += (int64_t)gridDim.x * NT) {
         const uint32_t t = (uint32_t)t64;
         int slot = -1, pos = 0;
         if (t < total) {
@@ -182,112 +183,154 @@ struct AppendParams {
     int *status;
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;   // token and head strides, elements
     int64_t page_stride, slot_stride, head_stride;
-    int64_t items;                                            // T * (Hq + 2 Hkv)
+    int64_t T;
     int Hq, Hkv, D, R, page, num_pos, num_slots;
-    float eps;
+    int lph, gpt, tpc;   // lanes a head, groups a token, tokens a CTA
+    float eps, inv_D;
+    Div by_page;
 };
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-template <>
-__device__ __forceinline__ float4 load4(const float *p) {
-    return *reinterpret_cast<const float4 *>(p);
+// V neighbouring entries in fp32 (V = 4, or 8 of fp16: 16-byte accesses but for 4 of fp16).
+template <int V>
+__device__ __forceinline__ void load_v(const float *p, float (&x)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + i);
+        x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+    }
 }
-template <>
-__device__ __forceinline__ float4 load4(const half *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = __half22float2(u32_as_h2(u.x)), b = __half22float2(u32_as_h2(u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
+template <int V>
+__device__ __forceinline__ void load_v(const half *p, float (&x)[V]) {
+    uint32_t u[V / 2];
+    if constexpr (V == 8) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        u[0] = v.x, u[1] = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; i++) {
+        const float2 f = __half22float2(u32_as_h2(u[i]));
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
 }
-__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void store4(half *p, float4 v) {
-    uint2 u;
-    u.x = h2_as_u32(__floats2half2_rn(v.x, v.y));
-    u.y = h2_as_u32(__floats2half2_rn(v.z, v.w));
-    *reinterpret_cast<uint2 *>(p) = u;
+template <int V>
+__device__ __forceinline__ void store_v(float *p, const float (&x)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<float4 *>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+}
+template <int V>
+__device__ __forceinline__ void store_v(half *p, const float (&x)[V]) {
+    uint32_t u[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; i++)
+        u[i] = h2_as_u32(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
+    if constexpr (V == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    else
+        *reinterpret_cast<uint2 *>(p) = make_uint2(u[0], u[1]);
 }
 
-__device__ __forceinline__ float dot4(float4 a) { return a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w; }
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
-__device__ __forceinline__ float4 mul4(float4 a, float s) { return make_float4(a.x * s, a.y * s, a.z * s, a.w * s); }
+// A group of `lph` lanes (a power of two, up to a warp) per head, 2 V entries a
+// lane: a rotary lane holds V entries of the first half and their V partners of
+// the second, so norm, rotation and store stay in registers; one rounding, at the
+// store.  A token's heads are spread over `gpt` groups of one CTA, so its slot,
+// position, cosines and sines are loaded once for the heads that a group takes.
+// Bound by bandwidth for many tokens, by the chain slot / position -> cosines ->
+// store for few.
+constexpr int kAppendThreads = 256;
 
-// One group of LPH lanes per (token, head), eight entries a lane: a rotary lane
-// holds four entries of the first half and their four partners of the second,
-// so norm, rotation and store stay in registers.  One rounding, at the store.
-template <typename T, int LPH>
-__global__ void __launch_bounds__(256) rope_append_kernel(const __grid_constant__ AppendParams p) {
+template <typename T, int V>
+__global__ void __launch_bounds__(kAppendThreads, V == 8 ? 4 : 6) rope_append_kernel(const __grid_constant__ AppendParams p) {
     pdl_wait();
     pdl_launch_dependents();
-    const int l = threadIdx.x % LPH;
-    const unsigned mask = LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1) << ((threadIdx.x & 31) / LPH * LPH);
+    const int l = threadIdx.x & (p.lph - 1), group = threadIdx.x / p.lph;
+    const unsigned mask = (p.lph == 32 ? 0xffffffffu : (1u << p.lph) - 1) << (threadIdx.x & 31 & ~(p.lph - 1));
+    const int tok = group / p.gpt, h0 = group - tok * p.gpt;
+    const int64_t t = (int64_t)blockIdx.x * p.tpc + tok;
+    if (tok >= p.tpc || t >= p.T)
+        return;
     const int heads = p.Hq + 2 * p.Hkv;
-    const int64_t step = (int64_t)gridDim.x * (256 / LPH);
-    const bool live = l * 8 < p.D;
-    const bool rot = l * 8 < p.R;
-    const int e0 = rot ? 4 * l : 8 * l, e1 = rot ? p.R / 2 + 4 * l : 8 * l + 4;
-    for (int64_t i = (int64_t)blockIdx.x * (256 / LPH) + threadIdx.x / LPH; i < p.items; i += step) {
-        const int64_t t = i / heads;
-        int h = (int)(i - t * heads);
-        const T *src;
-        T *dst = nullptr;
-        const float *w = nullptr;
-        bool turn = p.R > 0;
-        const int slot = p.slots[t];
-        const int pos = p.R > 0 ? p.pos[t] : 0;
-        const bool pos_ok = p.R == 0 || (pos >= 0 && pos < p.num_pos);
-        if (h < p.Hq) {
-            src = (const T *)p.q + t * p.q_ts + h * p.q_hs;
-            dst = (T *)p.q_out + t * p.o_ts + h * p.o_hs;
-            w = p.qw;
-        } else {
-            h -= p.Hq;
-            const bool is_v = h >= p.Hkv;
-            if (is_v)
-                h -= p.Hkv;
-            src = is_v ? (const T *)p.v + t * p.v_ts + h * p.v_hs : (const T *)p.k + t * p.k_ts + h * p.k_hs;
-            w = is_v ? nullptr : p.kw;
-            turn = turn && !is_v;
-            if (slot >= 0 && slot < p.num_slots && pos_ok) {
-                const int page = slot / p.page;
-                dst = (T *)(is_v ? p.v_cache : p.k_cache) + page * p.page_stride +
-                      (int64_t)(slot - page * p.page) * p.slot_stride + h * p.head_stride;
-            }
-            if (l == 0 && p.status && (slot < -1 || slot >= p.num_slots || !pos_ok))
-                atomicOr(p.status, 1);
-        }
-        float4 a = make_float4(0, 0, 0, 0), b = a;
+    const bool live = l * 2 * V < p.D, rot = l * 2 * V < p.R;
+    const int e0 = rot ? V * l : 2 * V * l, e1 = rot ? p.R / 2 + V * l : 2 * V * l + V;
+    // What no other load decides on is requested first: slot, position and the first head.
+    const int slot = p.slots[t];
+    const int pos = p.R > 0 ? p.pos[t] : 0;
+    float a[V], b[V];
+    auto load = [&](int i) {
+        const bool q = i < p.Hq, k = i < p.Hq + p.Hkv;
+        const int64_t ts = q ? p.q_ts : k ? p.k_ts : p.v_ts, hs = q ? p.q_hs : k ? p.k_hs : p.v_hs;
+        const T *src = (const T *)(q ? p.q : k ? p.k : p.v) + t * ts + (q ? i : k ? i - p.Hq : i - p.Hq - p.Hkv) * hs;
         if (live) {
-            a = load4(src + e0);
-            b = load4(src + e1);
-        }
-        if (w) {
-            float ss = dot4(a) + dot4(b);
+            load_v<V>(src + e0, a);
+            load_v<V>(src + e1, b);
+        } else {
 #pragma unroll
-            for (int o = LPH / 2; o; o >>= 1)
+            for (int j = 0; j < V; j++)
+                a[j] = b[j] = 0.0f;
+        }
+    };
+    load(h0);
+    const bool pos_ok = p.R == 0 || (pos >= 0 && pos < p.num_pos);
+    float c[V], s[V];
+    if (rot && pos_ok) {
+        load_v<V>(p.cos + (int64_t)pos * (p.R / 2) + V * l, c);
+        load_v<V>(p.sin + (int64_t)pos * (p.R / 2) + V * l, s);
+    }
+    const bool slot_ok = slot >= 0 && slot < p.num_slots && pos_ok;
+    if (h0 == 0 && l == 0 && p.status && (slot < -1 || slot >= p.num_slots || !pos_ok))
+        atomicOr(p.status, 1);
+    int64_t cache_at = 0;
+    if (slot_ok) {
+        const int page = quotient(slot, p.by_page);
+        cache_at = page * p.page_stride + (int64_t)(slot - page * p.page) * p.slot_stride;
+    }
+    for (int i = h0;;) {
+        const int kind = i < p.Hq ? 0 : i < p.Hq + p.Hkv ? 1 : 2;   // q, k, v
+        const float *w = kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr;
+        if (w) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; j++)
+                ss += a[j] * a[j] + b[j] * b[j];
+            for (int o = p.lph / 2; o; o >>= 1)
                 ss += __shfl_xor_sync(mask, ss, o);
-            const float r = 1.0f / sqrtf(ss / (float)p.D + p.eps);
+            const float r = rsqrtf(fmaf(ss, p.inv_D, p.eps));
             if (live) {
-                a = mul4(mul4(a, r), load4(w + e0));
-                b = mul4(mul4(b, r), load4(w + e1));
+                float x[V], y[V];
+                load_v<V>(w + e0, x);
+                load_v<V>(w + e1, y);
+#pragma unroll
+                for (int j = 0; j < V; j++)
+                    a[j] = a[j] * r * x[j], b[j] = b[j] * r * y[j];
             }
         }
-        if (!dst || !live)
-            continue;
-        if (turn && rot) {
-            if (pos_ok) {
-                const float4 c = load4(p.cos + (int64_t)pos * (p.R / 2) + 4 * l);
-                const float4 s = load4(p.sin + (int64_t)pos * (p.R / 2) + 4 * l);
-                const float4 x = a, y = b;
-                a = make_float4(x.x * c.x - y.x * s.x, x.y * c.y - y.y * s.y, x.z * c.z - y.z * s.z,
-                                x.w * c.w - y.w * s.w);
-                b = make_float4(y.x * c.x + x.x * s.x, y.y * c.y + x.y * s.y, y.z * c.z + x.z * s.z,
-                                y.w * c.w + x.w * s.w);
+        if (rot && kind < 2 && pos_ok) {
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                const float x = a[j], y = b[j];
+                a[j] = x * c[j] - y * s[j];
+                b[j] = y * c[j] + x * s[j];
             }
         }
-        if (!pos_ok)
-            a = b = make_float4(0, 0, 0, 0);   // only a q row: a k or v row has no dst then
-        store4(dst + e0, a);
-        store4(dst + e1, b);
+        if (!pos_ok) {   // a zero q row; k and v are dropped
+#pragma unroll
+            for (int j = 0; j < V; j++)
+                a[j] = b[j] = 0.0f;
+        }
+        if (live && (kind == 0 || slot_ok)) {
+            const int64_t hs = kind == 0 ? p.o_hs : p.head_stride;
+            T *dst = (T *)(kind == 0 ? p.q_out : kind == 1 ? p.k_cache : p.v_cache) + (kind == 0 ? t * p.o_ts : cache_at) +
+                     (kind == 0 ? i : kind == 1 ? i - p.Hq : i - p.Hq - p.Hkv) * hs;
+            store_v<V>(dst + e0, a);
+            store_v<V>(dst + e1, b);
+        }
+        i += p.gpt;
+        if (i >= heads)
+            return;
+        load(i);
     }
 }
 
@@ -312,13 +355,20 @@ int launch(const char *fn, void (*kernel)(P), const P &p, int grid, int threads,
     return MNB_OK;
 }
 
-template <typename T>
-int launch_append(const AppendParams &p, unsigned flags, cudaStream_t s) {
-    const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
-    const int64_t ctas = (p.items * lanes + 255) / 256;
-    const int grid = (int)(ctas < device_sm_count() * 64 ? ctas : device_sm_count() * 64);
-    auto *k = lanes == 8 ? rope_append_kernel<T, 8> : lanes == 16 ? rope_append_kernel<T, 16> : rope_append_kernel<T, 32>;
-    return launch("mnb_rope_append", k, p, grid, 256, 0, flags, s);
+template <typename T, int V>
+int launch_append(AppendParams p, unsigned flags, cudaStream_t s) {
+    const int heads = p.Hq + 2 * p.Hkv, units = (p.D + 2 * V - 1) / (2 * V);
+    p.lph = 1;
+    while (p.lph < units)
+        p.lph *= 2;
+    const int groups = kAppendThreads / p.lph;
+    const int rounds = (heads + groups - 1) / groups;
+    p.gpt = (heads + rounds - 1) / rounds;   // as many heads a group for all groups, or one fewer
+    p.tpc = groups / p.gpt;
+    if (p.T < p.tpc)
+        p.tpc = (int)p.T;
+    const int threads = (p.tpc * p.gpt * p.lph + 31) / 32 * 32;
+    return launch("mnb_rope_append", rope_append_kernel<T, V>, p, (int)((p.T + p.tpc - 1) / p.tpc), threads, 0, flags, s);
 }
 
 }  // namespace
@@ -332,11 +382,14 @@ int launch_paged_tables(const int32_t *ctx, const int32_t *neu, int B, int page,
     p.table = table, p.seq = seq, p.cu = cu, p.slots = slots, p.pos = pos, p.free_next = free_next;
     p.status = status, p.table_stride = table_stride;
     p.B = B, p.page = page, p.max_blocks = max_blocks, p.T = T, p.num_free = num_free, p.num_pages = num_pages;
-    const int by_tokens = (T + kTabThreads - 1) / kTabThreads, by_rows = (B + kTabThreads / 32 - 1) / (kTabThreads / 32);
+    // a short barrier for a decode step's few requests, wide scans for many
+    const int nt = B <= 128 && T <= 1024 ? 128 : 512;
+    const int by_tokens = (T + nt - 1) / nt, by_rows = (B + nt / 32 - 1) / (nt / 32);
     int grid = by_tokens > by_rows ? by_tokens : by_rows;
     const int most = device_sm_count() * 2;
     grid = grid < 1 ? 1 : grid > most ? most : grid;
-    return launch("mnb_paged_tables", paged_tables_kernel, p, grid, kTabThreads, (size_t)(2 * B + 1) * 4, flags, s);
+    return launch("mnb_paged_tables", nt == 128 ? paged_tables_kernel<128> : paged_tables_kernel<512>, p, grid, nt,
+                  (size_t)(2 * B + 1) * 4, flags, s);
 }
 
 int launch_rope_append(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs,
@@ -349,10 +402,13 @@ int launch_rope_append(const void *q, int64_t q_ts, int64_t q_hs, const void *k,
     p.slots = slots, p.pos = pos, p.cos = cos, p.sin = sin, p.qw = qw, p.kw = kw, p.status = status;
     p.q_ts = q_ts, p.q_hs = q_hs, p.k_ts = k_ts, p.k_hs = k_hs, p.v_ts = v_ts, p.v_hs = v_hs, p.o_ts = o_ts, p.o_hs = o_hs;
     p.page_stride = c->page_stride, p.slot_stride = c->slot_stride, p.head_stride = c->head_stride;
-    p.items = T * (Hq + 2 * c->num_heads);
+    p.T = T;
     p.Hq = Hq, p.Hkv = (int)c->num_heads, p.D = (int)c->head_dim, p.R = R, p.page = (int)c->page_size;
+    p.inv_D = 1.0f / (float)p.D, p.by_page = div_by((uint32_t)c->page_size);
     p.num_pos = num_pos, p.num_slots = (int)(c->num_pages * c->page_size), p.eps = eps;
-    return c->dtype == MNB_F16 ? launch_append<half>(p, flags, s) : launch_append<float>(p, flags, s);
+    if (c->dtype == MNB_F32)
+        return launch_append<float, 4>(p, flags, s);
+    return p.D % 16 == 0 && R % 16 == 0 ? launch_append<half, 8>(p, flags, s) : launch_append<half, 4>(p, flags, s);
 }
 
 }  // namespace mnb
