@@ -10,11 +10,14 @@ of libmnb, optionally captured into a CUDA graph.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (MNB_FLAG_PDL, mnb_dequantize, mnb_embed_gather, mnb_gemm, mnb_gemv, mnb_gemv_argmax,
                mnb_gemv_argmax_workspace_bytes, mnb_gemv_chain, mnb_gemv_chain_plan, mnb_gemv_chain_workspace_bytes,
-               mnb_gemv_swiglu, mnb_matmul, mnb_packed_sizes, mnb_quantize_rtn)
+               mnb_gemv_swiglu, mnb_matmul, mnb_packed_sizes, mnb_paged_attention, mnb_paged_attention_workspace_bytes,
+               mnb_paged_tables, mnb_quantize_rtn, mnb_rope_append)
 
 
 class QLinear:
@@ -118,6 +121,92 @@ def fuse_decoder(linears, swiglu=False):
     return out
 
 
+class PagedCache:
+    """Keys and values of a decoder's layers in pages, for up to `requests` requests at once.
+
+    The requests' lengths, their block table and the list of free pages live on the
+    device and advance there, so a captured step can be replayed token after token:
+    begin() hands out the pages and slots of the step's new tokens (mnb_paged_tables),
+    layer() appends one layer's keys and values (mnb_rope_append) and attends over them
+    (mnb_paged_attention), end() makes the new lengths current.  All layers share the
+    table; each has a pool of its own, [pages, page_size, Hkv, D].
+
+    cos, sin: fp32 [max_len, rot_dim / 2] (None: no rotation).  norms: per layer a pair
+    of fp32 [D] RMS-norm weights of q and k, or None.  status: the device word that the
+    three calls report to; check() reads it.
+    """
+
+    def __init__(self, layers, requests, Hq, Hkv, D, max_len, page_size=16, pages=None, dtype=torch.float16,
+                 cos=None, sin=None, norms=None, eps=1e-6, scale=None, device="cuda"):
+        self.requests, self.Hq, self.Hkv, self.D = requests, Hq, Hkv, D
+        self.page_size, self.cos, self.sin, self.norms, self.eps = page_size, cos, sin, norms, eps
+        self.scale = D ** -0.5 if scale is None else scale
+        blocks = -(-max_len // page_size)
+        self.pages = requests * blocks if pages is None else pages
+        self.k, self.v = ([torch.zeros((self.pages, page_size, Hkv, D), dtype=dtype, device=device)
+                           for _ in range(layers)] for _ in range(2))
+
+        def i32(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=device)
+
+        self.table, self.lens, self.new_lens = i32(requests, blocks), i32(requests), i32(requests)
+        self.cu_new, self.one, self.status = i32(requests + 1), i32(requests) + 1, i32(1)
+        self.free = torch.arange(self.pages, dtype=torch.int32, device=device)
+        self.start, self.next = i32(1), i32(1)
+        # a decode step's slots and positions, and its rotated queries
+        self.slots, self.positions = i32(requests), i32(requests)
+        self.q = torch.zeros((requests, Hq, D), dtype=dtype, device=device)
+        self.ws = torch.zeros((mnb_paged_attention_workspace_bytes(requests, Hq, Hkv, D, dtype),), dtype=torch.uint8,
+                              device=device)
+
+    launches_per_step = 1            # begin(); end() is two copies
+    launches_per_layer = 2
+
+    def begin(self, new=None, slots=None, positions=None, flags=0, stream=None):
+        """Pages and slots of new [requests] more tokens a request (None: one each, a decode step), the slots and
+        positions of the new tokens in buffers of the caller's then."""
+        slots, positions = (self.slots, self.positions) if slots is None else (slots, positions)
+        mnb_paged_tables(self.lens, self.one if new is None else new, self.table, self.page_size, self.pages,
+                         self.free, self.start, self.new_lens, self.cu_new, slots, positions, self.next, self.status,
+                         flags, stream)
+
+    def append(self, layer, q, k, v, q_out, slots=None, positions=None, flags=0, stream=None):
+        """q [T, Hq, D] normed and rotated into q_out, k and v [T, Hkv, D] into the layer's pools."""
+        slots, positions = (self.slots, self.positions) if slots is None else (slots, positions)
+        qw, kw = (None, None) if self.norms is None else self.norms[layer]
+        mnb_rope_append(q, k, v, self.k[layer], self.v[layer], slots, positions, self.cos, self.sin, q_out, qw, kw,
+                        self.eps, self.status, flags, stream)
+
+    def layer(self, layer, q, k, v, out, flags=0, stream=None):
+        """One layer of a decode step: out [requests, Hq, D] from this step's q, k and v."""
+        self.append(layer, q, k, v, self.q, flags=flags, stream=stream)
+        mnb_paged_attention(self.q, self.k[layer], self.v[layer], self.table, self.new_lens, self.scale, out, self.ws,
+                            None, self.status, flags, stream)
+
+    def end(self, stream=None):
+        """The step's lengths and free-list position become current."""
+        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext():
+            self.lens.copy_(self.new_lens)
+            self.start.copy_(self.next)
+
+    def state(self):
+        """Lengths, free-list position and status, to be given to restore(): steps in between are then undone (their
+        pages go back to the list; the rows they wrote are written again by the next steps)."""
+        return [t.clone() for t in (self.lens, self.start, self.status)]
+
+    def restore(self, state):
+        for t, was in zip((self.lens, self.start, self.status), state):
+            t.copy_(was)
+
+    def check(self):
+        """Raises if a step since the last check met a bad index, a request without room or an empty free list
+        (synchronizes)."""
+        word = int(self.status.item())
+        self.status.zero_()
+        if word:
+            raise RuntimeError(f"paged cache: status {word} (1 a bad index, 2 a length without room, 4 no free page)")
+
+
 class Pass:
     """A chain of MatMulNBits calls with one X / Y buffer pair per linear.
 
@@ -126,10 +215,15 @@ class Pass:
     launch may overlap the tail of the previous one (weights stream early, X is
     read after the previous kernel completes).  An optional int8 embedding
     gather of M token ids runs first, as in a decode step.
+
+    attention: a PagedCache for M requests.  The pass is then a decode step whose
+    attention runs too: after each layer's v (or fused qkv) projection, q, k and v
+    go through PagedCache.layer, whose result is the input of that layer's o
+    projection, and every run appends one token to each request.
     """
 
     def __init__(self, linears, M, kind="gemv", act_dtype=torch.float16, pdl=True, embed=None, greedy=False,
-                 chain=False, waits=None):
+                 chain=False, waits=None, attention=None):
         self.linears, self.M, self.kind, self.pdl = list(linears), M, kind, pdl
         dev = self.linears[0].packed.device
         # one flat buffer each for all inputs and all outputs (views per linear,
@@ -169,6 +263,28 @@ class Pass:
             self.chain = (plan, plan.to(dev),
                           torch.zeros((mnb_gemv_chain_workspace_bytes(n),), dtype=torch.uint8, device=dev))
 
+        self.attention = attention
+        if attention is not None:
+            assert self.chain is None and attention.requests == M and attention.q.dtype == act_dtype
+            self.layers = self._attention_layers()   # {index of the v or qkv projection: (layer, q, k, v, out)}
+
+    def _attention_layers(self):
+        c, at, found = self.attention, {l.name: i for i, l in enumerate(self.linears)}, {}
+        nq, nk = c.Hq * c.D, c.Hkv * c.D
+        for layer in range(len(c.k)):
+            if f"qkv{layer}" in at:
+                last = at[f"qkv{layer}"]
+                q, k, v = self.Y[last].split([nq, nk, nk], dim=1)
+            else:
+                q, k, v = (self.Y[at[f"{n}{layer}"]] for n in "qkv")
+                last = max(at[f"{n}{layer}"] for n in "qkv")
+            o = at[f"o{layer}"]
+            assert last < o and self.linears[o].K == nq
+            heads = [t.view(self.M, -1, c.D) for t in (q, k, v, self.X[o])]
+            assert [t.shape[1] for t in heads] == [c.Hq, c.Hkv, c.Hkv, c.Hq]
+            found[last] = (layer, *heads)
+        return found
+
     @property
     def weight_bytes(self):
         return sum(l.nbytes for l in self.linears)
@@ -180,6 +296,8 @@ class Pass:
     @property
     def launches(self):
         n = 1 if self.chain is not None else len(self.linears)
+        if self.attention is not None:
+            n += self.attention.launches_per_step + len(self.layers) * self.attention.launches_per_layer
         return n + (1 if self.embed is not None else 0)
 
     def run(self, stream=None):
@@ -192,6 +310,8 @@ class Pass:
             mnb_gemv_chain(*self.chain, flags, stream)
             return
         last = len(self.linears) - 1
+        if self.attention is not None:
+            self.attention.begin(flags=0, stream=stream)   # after the copies that ended the last step
         for i, (l, x, y) in enumerate(zip(self.linears, self.X, self.Y)):
             if self.kind == "gemv":
                 if self.greedy and i == last:
@@ -204,13 +324,20 @@ class Pass:
                 l.matmul(x, y, flags, stream)
             else:
                 l.gemm(x, y, flags, stream)
+            if self.attention is not None and i in self.layers:
+                self.attention.layer(*self.layers[i], flags=flags, stream=stream)
+        if self.attention is not None:
+            self.attention.end(stream)
 
     def capture(self):
         """Capture run() into a CUDA graph (replayed with replay())."""
         s = torch.cuda.Stream()
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
+            state = None if self.attention is None else self.attention.state()
             self.run(s)          # warm-up outside the graph (first-use attribute setup)
+            if state is not None:
+                self.attention.restore(state)   # the warm-up's tokens are no step of the user's
         torch.cuda.current_stream().wait_stream(s)
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()

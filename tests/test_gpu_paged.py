@@ -501,3 +501,70 @@ def test_captured_step_follows_its_lengths(mnb, cuda_dev):
     lens = st["seq"].cpu()
     case = (q_out.cpu(), st["kc"].cpu(), st["vc"].cpu(), st["table"].cpu(), lens)
     assert_attn(out.cpu(), None, case, 0.09)
+
+
+@pytest.mark.parametrize("fused,kind,dtype", [(True, "gemv", F16), (False, "gemv", F16), (False, "matmul", F32)])
+def test_pass_with_attention(mnb, cuda_dev, fused, kind, dtype):
+    """step.Pass with a PagedCache: two layers, three requests, prompts and then captured steps.  Each step's o inputs
+    against the 64-bit attention over all q, k and v that the projections have put out so far."""
+    from int4_block_quantized_matmulnbits_b200 import step
+
+    M, hidden, Hq, H, D, ps, layers, steps = 3, 256, 4, 2, 64, 16, 2, 20
+    gen = torch.Generator().manual_seed(7)
+    sdt = F16 if dtype == F16 else F32
+    lin = []
+    for layer in range(layers):
+        for name, N, K in (("q", Hq * D, hidden), ("k", H * D, hidden), ("v", H * D, hidden), ("o", hidden, Hq * D)):
+            W = (torch.randn(N, K, generator=gen) * 0.06).to(cuda_dev)
+            lin.append(step.QLinear.quantize(W, 32, True, sdt, name=f"{name}{layer}"))
+        if fused:
+            lin[-4:] = [step.concat_linears(lin[-4:-1], f"qkv{layer}"), lin[-1]]
+    prompt = [5, 33, 16]
+    ang = torch.rand(64, D // 2, generator=gen, dtype=torch.float64) * 100
+    cos, sin = ang.cos().float().to(cuda_dev), ang.sin().float().to(cuda_dev)
+    norms = [tuple((1 + 0.2 * torch.randn(D, generator=gen)).to(cuda_dev) for _ in range(2)) for _ in range(layers)]
+    cache = step.PagedCache(layers, M, Hq, H, D, 64, ps, dtype=dtype, cos=cos, sin=sin, norms=norms)
+    p = step.Pass(lin, M, kind, dtype, attention=cache)
+    assert p.launches == len(lin) + 1 + 2 * layers
+    x = torch.randn(p.x_flat.shape, generator=gen).to(dtype)
+    p.x_flat.copy_(x)
+    p.capture()
+    assert cache.lens.cpu().tolist() == [0] * M and int(cache.start) == 0   # its warm-up left no token behind
+    # the prompts
+    T = sum(prompt)
+    slots, pos = torch.empty(T, dtype=torch.int32, device=cuda_dev), torch.empty(T, dtype=torch.int32, device=cuda_dev)
+    cache.begin(_i32(prompt, cuda_dev), slots, pos)
+    ks, vs = [], []                   # per layer, per request: the rows of the cache so far
+    for layer in range(layers):
+        qkv = torch.randn(T, (Hq + 2 * H) * D, generator=gen).to(dtype)
+        q, k, v = split_qkv(qkv.to(cuda_dev), Hq, H, D)
+        cache.append(layer, q, k, v, torch.empty_like(q, memory_format=torch.contiguous_format), slots, pos)
+        kr = turn_ref(k.cpu(), norms[layer][1].cpu(), 1e-6, cos.cpu(), sin.cpu(), pos.cpu()).to(dtype)
+        ks.append(list(kr.split(prompt))), vs.append(list(v.cpu().split(prompt)))
+    cache.end()
+    for i in range(steps):
+        x = torch.randn(p.x_flat.shape, generator=gen).to(dtype)
+        p.x_flat.copy_(x)
+        p.replay()
+        torch.cuda.synchronize()
+        cache.check()
+        at = torch.tensor([n + i for n in prompt])
+        assert cache.lens.cpu().tolist() == (at + 1).tolist()
+        for last, (layer, q, k, v, out) in p.layers.items():
+            kr = turn_ref(k.cpu(), norms[layer][1].cpu(), 1e-6, cos.cpu(), sin.cpu(), at).to(dtype)
+            qr = turn_ref(q.cpu(), norms[layer][0].cpu(), 1e-6, cos.cpu(), sin.cpu(), at).to(dtype)
+            for b in range(M):
+                ks[layer][b] = torch.cat([ks[layer][b], kr[b:b + 1]])
+                vs[layer][b] = torch.cat([vs[layer][b], v[b:b + 1].cpu()])
+            width = ceil_div(max(prompt) + i + 1, ps)
+            kd, vd = torch.zeros(M * width, ps, H, D, dtype=dtype), torch.zeros(M * width, ps, H, D, dtype=dtype)
+            for b in range(M):
+                kd[b * width:(b + 1) * width].view(-1, H, D)[:at[b] + 1] = ks[layer][b]
+                vd[b * width:(b + 1) * width].view(-1, H, D)[:at[b] + 1] = vs[layer][b]
+            tab = torch.arange(M * width, dtype=torch.int32).view(M, width)
+            ref, rl, spread, reach = attn_ref(qr, kd, vd, tab, at + 1, D ** -0.5)
+            t_out, _ = attn_tolerance(ref, rl, spread, reach, dtype, int(at.max()) + 1, D)
+            # q and k each within a step (2 u) of the reference's rounding: |ds| <= 4 u reach, as much again in p
+            u = 2.0 ** -11 if dtype == F16 else 2.0 ** -24
+            more = 4 * u * reach + 2 * (D / 2 + 8) * 2.0 ** -22 * reach
+            assert bool(((out.cpu().double() - ref).abs() <= t_out + 2 * more[..., None] * spread).all())
