@@ -388,6 +388,17 @@ typedef struct mnb_paged_cache {
     int32_t reserved;       /* 0 */
 } mnb_paged_cache;
 
+typedef struct mnb_paged_tables_args {
+    const int32_t *ctx_lens, *new_lens;      /* [B] */
+    const int32_t *free_pages, *free_start;  /* [num_free], [1] */
+    int32_t *block_table;                    /* [B] rows of max_blocks, table_stride apart */
+    int32_t *seq_lens, *cu_new;              /* [B], [B + 1] */
+    int32_t *slots, *positions;              /* [T] */
+    int32_t *free_next;                      /* [1] */
+    int *status;                             /* [1] or NULL */
+    int64_t B, T, page_size, num_pages, num_free, table_stride, max_blocks;
+} mnb_paged_tables_args;
+
 /* Block tables, slots and positions of a step's new tokens, on the GPU.
  * Request b holds ctx_lens[b] tokens and gets new_lens[b] more; the new tokens
  * of all requests stand one request behind the other.  Pages of request b:
@@ -411,12 +422,22 @@ typedef struct mnb_paged_cache {
  * Outputs must not overlap inputs (block_table is both).  0 <= B <= 4096.
  * Errors: MNB_ERR_INVALID_ARG, MNB_ERR_SHAPE, MNB_ERR_ALIGN,
  *         MNB_ERR_UNSUPPORTED (B > 4096), MNB_ERR_CUDA. */
-MNB_API int mnb_paged_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B, int64_t page_size,
-                             int64_t num_pages, const int32_t *free_pages, int64_t num_free,
-                             const int32_t *free_start, int32_t *block_table, int64_t table_stride,
-                             int64_t max_blocks, int32_t *seq_lens, int32_t *cu_new, int32_t *slots,
-                             int32_t *positions, int64_t T, int32_t *free_next, int *status, unsigned flags,
-                             void *stream);
+MNB_API int mnb_paged_tables(const mnb_paged_tables_args *args, unsigned flags, void *stream);
+
+typedef struct mnb_rope_append_args {
+    const void *q, *k, *v;                   /* [T][Hq][D], [T][Hkv][D] twice, at the strides below */
+    void *q_out;                             /* [T][Hq][D] */
+    const int32_t *slots, *positions;        /* [T] */
+    const float *cos, *sin;                  /* [num_pos][rot_dim / 2] */
+    const float *q_weight, *k_weight;        /* [D] or NULL */
+    int *status;                             /* [1] or NULL */
+    mnb_paged_cache cache;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;   /* elements */
+    int64_t v_token_stride, v_head_stride, o_token_stride, o_head_stride;
+    int64_t T, Hq, rot_dim, num_pos;
+    float eps;
+    int32_t reserved;                        /* 0 */
+} mnb_rope_append_args;
 
 /* The new tokens' q, k and v on their way into the attention and the cache.
  * For each token t, with c, s = rows positions[t] of the tables cos and sin
@@ -433,13 +454,23 @@ MNB_API int mnb_paged_tables(const int32_t *ctx_lens, const int32_t *new_lens, i
  * gives a zero q row and drops k and v (bit 0).  Two tokens must not have the
  * same slot.
  * Errors: MNB_ERR_INVALID_ARG, MNB_ERR_SHAPE, MNB_ERR_ALIGN, MNB_ERR_CUDA. */
-MNB_API int mnb_rope_append(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
-                            int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
-                            int64_t v_head_stride, const mnb_paged_cache *cache, const int32_t *slots,
-                            const int32_t *positions, int64_t T, int64_t Hq, const float *cos, const float *sin,
-                            int64_t rot_dim, int64_t num_pos, const float *q_weight, const float *k_weight,
-                            float eps, void *q_out, int64_t o_token_stride, int64_t o_head_stride, int *status,
-                            unsigned flags, void *stream);
+MNB_API int mnb_rope_append(const mnb_rope_append_args *args, unsigned flags, void *stream);
+
+typedef struct mnb_paged_attention_args {
+    const void *q;                           /* [B][Hq][D] at the strides below */
+    void *out;                               /* [B][Hq][D] */
+    float *lse;                              /* [B][Hq] or NULL */
+    const int32_t *block_table;              /* [B] rows of max_blocks, table_stride apart */
+    const int32_t *seq_lens;                 /* [B] */
+    void *workspace;
+    int *status;                             /* [1] or NULL */
+    mnb_paged_cache cache;
+    int64_t q_request_stride, q_head_stride, o_request_stride, o_head_stride;   /* elements */
+    int64_t table_stride, max_blocks, B, Hq;
+    size_t ws_bytes;
+    float scale;
+    int32_t reserved;                        /* 0 */
+} mnb_paged_attention_args;
 
 /* Attention of one new token per request over its pages (decode; grouped heads:
  * query head i reads KV head i / (Hq / Hkv)).  With n = seq_lens[b] and j < n,
@@ -463,11 +494,7 @@ MNB_API int mnb_rope_append(const void *q, int64_t q_token_stride, int64_t q_hea
  *         MNB_ERR_ALIGN, MNB_ERR_UNSUPPORTED, MNB_ERR_CUDA. */
 MNB_API size_t mnb_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
                                                    mnb_dtype dtype);   /* 0 for sizes the call refuses */
-MNB_API int mnb_paged_attention(const void *q, int64_t q_request_stride, int64_t q_head_stride,
-                                const mnb_paged_cache *cache, const int32_t *block_table, int64_t table_stride,
-                                int64_t max_blocks, const int32_t *seq_lens, int64_t B, int64_t Hq, float scale,
-                                void *out, int64_t o_request_stride, int64_t o_head_stride, float *lse,
-                                void *workspace, size_t ws_bytes, int *status, unsigned flags, void *stream);
+MNB_API int mnb_paged_attention(const mnb_paged_attention_args *args, unsigned flags, void *stream);
 
 /* Reads (and, if clear != 0, zeroes) the library's device status word on the
  * current device into *status_out: bit 0 = a GEMM or GEMV mbarrier wait timed

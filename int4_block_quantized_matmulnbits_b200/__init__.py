@@ -27,7 +27,7 @@ __all__ = [
     "mnb_gemv_argmax", "mnb_gemv_argmax_workspace_bytes", "mnb_gemv_argmax_noalloc", "mnb_gemv_swiglu",
     "mnb_gemv_task", "mnb_gemv_chain_plan_bytes", "mnb_gemv_chain_workspace_bytes", "mnb_gemv_chain_plan",
     "mnb_gemv_chain", "mnb_matmul", "mnb_gptq_hessian", "mnb_gptq_workspace_bytes", "mnb_gptq_prepare",
-    "mnb_gptq_quantize", "mnb_paged_cache", "mnb_paged_tables", "mnb_rope_append", "mnb_paged_attention",
+    "mnb_gptq_quantize", "mnb_paged_tables", "mnb_rope_append", "mnb_paged_attention",
     "mnb_paged_attention_workspace_bytes",
 ]
 
@@ -51,14 +51,6 @@ class mnb_gemv_task(ctypes.Structure):
     _fields_ = [("X", ctypes.c_void_p), ("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("zp", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("wait", ctypes.c_int32), ("reserved", ctypes.c_int32)]
-
-
-class mnb_paged_cache(ctypes.Structure):
-    """The pool of a paged key-value cache (the C struct of the same name)."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
-                ("page_size", ctypes.c_int64), ("num_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
-                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def _load():
@@ -93,13 +85,10 @@ def _load():
         "mnb_gptq_workspace_bytes": ([i64], sz),
         "mnb_gptq_prepare": ([vp, i64, ctypes.c_float, vp, vp, vp, sz, P(ctypes.c_float), vp], i32),
         "mnb_gptq_quantize": ([vp, vp, vp, i64, i64, i32, i32, vp, vp, i32, vp, vp], i32),
-        "mnb_paged_tables": ([vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, i64, vp, vp, u32, vp],
-                             i32),
-        "mnb_rope_append": ([vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp, i64, i64, vp, vp,
-                             i64, i64, vp, vp, ctypes.c_float, vp, i64, i64, vp, u32, vp], i32),
+        "mnb_paged_tables": ([vp, u32, vp], i32),
+        "mnb_rope_append": ([vp, u32, vp], i32),
         "mnb_paged_attention_workspace_bytes": ([i64, i64, i64, i64, i32], sz),
-        "mnb_paged_attention": ([vp, i64, i64, vp, vp, i64, i64, vp, i64, i64, ctypes.c_float, vp,
-                                 i64, i64, vp, vp, sz, vp, u32, vp], i32),
+        "mnb_paged_attention": ([vp, u32, vp], i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -325,7 +314,11 @@ def mnb_gptq_quantize(W, U, dead, bs, has_zp, packed, scales, zp, stream=None):
 # the checks that pass read each property of a tensor once and call no helper
 # per tensor; what a failed one has found is worked out afterwards, in _explain.
 
-_pack_cache = struct.Struct("@PPqqqqqqqii").pack   # mnb_paged_cache as bytes
+# The C structs of the same names as bytes: one conversion for all fields.
+_CACHE = "PPqqqqqqqii"
+_pack_tables = struct.Struct("@11P7q").pack                            # mnb_paged_tables_args
+_pack_append = struct.Struct("@11P" + _CACHE + "12qfi").pack           # mnb_rope_append_args
+_pack_attention = struct.Struct("@7P" + _CACHE + "8qNfi").pack         # mnb_paged_attention_args
 _PAGED_DT = {torch.float16: MNB_F16, torch.float32: MNB_F32}
 
 
@@ -394,11 +387,11 @@ def mnb_paged_tables(ctx_lens, new_lens, block_table, page_size, num_pages, free
                  cu_new=(cu_new, i32, (B + 1,), "flat"), slots=(slots, i32, (T,), "flat"),
                  positions=(positions, i32, (T,), "flat"), free_next=(free_next, i32, (1,), "flat"),
                  status=(status, i32, (1,), "flat"))
-    rc = _lib.mnb_paged_tables(
-        ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size, num_pages, free_pages.data_ptr(), F,
-        free_start.data_ptr(), block_table.data_ptr(), stride if B > 1 else blocks, blocks, seq_lens.data_ptr(),
-        cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(), T, free_next.data_ptr(),
-        None if status is None else status.data_ptr(), flags, _raw_stream(dev) if stream is None else _stream(stream))
+    rc = _lib.mnb_paged_tables(_pack_tables(
+        ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_start.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+        free_next.data_ptr(), 0 if status is None else status.data_ptr(), B, T, page_size, num_pages, F,
+        stride if B > 1 else blocks, blocks), flags, _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(fn, rc)
 
@@ -428,7 +421,7 @@ def mnb_rope_append(q, k, v, k_cache, v_cache, slots, positions, cos, sin, q_out
         ks, vs = k.stride(), v.stride()
         ok = (ks[2] == 1 and vs[2] == 1) or T * D <= 1
     Hq = half = num_pos = 0
-    qp = op = cp = sp = pp = qwp = kwp = None
+    qp = op = cp = sp = pp = qwp = kwp = 0
     if q is not None:
         Hq = q.shape[1] if q.dim() == 3 else -1
         rows = (T, Hq, D)
@@ -462,11 +455,11 @@ def mnb_rope_append(q, k, v, k_cache, v_cache, slots, positions, cos, sin, q_out
                  positions=(positions, i32, (T,), "flat"), cos=(cos, f32, (num_pos, half), "flat"),
                  sin=(sin, f32, (num_pos, half), "flat"), q_weight=(q_weight, f32, (D,), "flat"),
                  k_weight=(k_weight, f32, (D,), "flat"), status=(status, i32, (1,), "flat"))
-    cache = _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), P, ps, H, D, strides[0], strides[1], strides[2], dt, 0)
-    rc = _lib.mnb_rope_append(
-        qp, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], cache, slots.data_ptr(), pp, T, Hq,
-        cp, sp, 2 * half, num_pos, qwp, kwp, eps, op, os_[0], os_[1], None if status is None else status.data_ptr(),
-        flags, _raw_stream(dev) if stream is None else _stream(stream))
+    rc = _lib.mnb_rope_append(_pack_append(
+        qp, k.data_ptr(), v.data_ptr(), op, slots.data_ptr(), pp, cp, sp, qwp, kwp,
+        0 if status is None else status.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), P, ps, H, D, strides[0],
+        strides[1], strides[2], dt, 0, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], T, Hq, 2 * half,
+        num_pos, eps, 0), flags, _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(fn, rc)
 
@@ -512,11 +505,11 @@ def mnb_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, 
                  block_table=(block_table, i32, (B, blocks), "rows"), seq_lens=(seq_lens, i32, (B,), "flat"),
                  workspace=(workspace, torch.uint8, (workspace.numel(),), "flat"),
                  lse=(lse, torch.float32, (B, Hq), "flat"), status=(status, i32, (1,), "flat"))
-    cache = _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), P, ps, H, D, strides[0], strides[1], strides[2], dt, 0)
-    rc = _lib.mnb_paged_attention(
-        q.data_ptr(), qs[0], qs[1], cache, block_table.data_ptr(), table_stride if B > 1 else blocks, blocks,
-        seq_lens.data_ptr(), B, Hq, scale, out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), None if status is None else status.data_ptr(), flags,
+    rc = _lib.mnb_paged_attention(_pack_attention(
+        q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), workspace.data_ptr(), 0 if status is None else status.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), P, ps, H, D, strides[0], strides[1], strides[2], dt, 0, qs[0], qs[1], os_[0], os_[1],
+        table_stride if B > 1 else blocks, blocks, B, Hq, workspace.numel(), scale, 0), flags,
         _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(fn, rc)

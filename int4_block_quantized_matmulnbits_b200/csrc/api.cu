@@ -137,8 +137,6 @@ static int check_stride(const char *fn, int64_t stride, int dtype) {
 // Checks *given and copies it to *c, the strides of single extents as 0.
 static int check_paged_cache(const char *fn, const mnb_paged_cache *given, mnb_paged_cache *c) {
     int rc;
-    if (!given)
-        return fail(MNB_ERR_INVALID_ARG, "%s: NULL cache", fn);
     *c = *given;
     if (c->num_pages == 1)
         c->page_stride = 0;
@@ -509,53 +507,62 @@ int mnb_gptq_quantize(const float *W, const float *U, const uint8_t *dead, int64
                                 has_zp ? zp : nullptr, (cudaStream_t)stream);
 }
 
-int mnb_paged_tables(const int32_t *ctx_lens, const int32_t *new_lens, int64_t B, int64_t page_size,
-                     int64_t num_pages, const int32_t *free_pages, int64_t num_free, const int32_t *free_start,
-                     int32_t *block_table, int64_t table_stride, int64_t max_blocks, int32_t *seq_lens,
-                     int32_t *cu_new, int32_t *slots, int32_t *positions, int64_t T, int32_t *free_next, int *status,
-                     unsigned flags, void *stream) {
+int mnb_paged_tables(const mnb_paged_tables_args *args, unsigned flags, void *stream) {
     clear_error();
     const char *fn = "mnb_paged_tables";
-    if (B < 0 || T < 0 || num_free < 0)
-        return fail(MNB_ERR_INVALID_ARG, "%s: negative size (B=%lld T=%lld num_free=%lld)", fn, (long long)B,
-                    (long long)T, (long long)num_free);
-    if (B > kMaxRequests)
-        return fail(MNB_ERR_UNSUPPORTED, "%s: B=%lld above %lld", fn, (long long)B, (long long)kMaxRequests);
-    if (page_size < 1 || num_pages < 1 || page_size > kMaxSlots || num_pages > kMaxSlots / page_size)
+    if (!args)
+        return fail(MNB_ERR_INVALID_ARG, "%s: NULL arguments", fn);
+    const mnb_paged_tables_args &a = *args;
+    if (a.B < 0 || a.T < 0 || a.num_free < 0)
+        return fail(MNB_ERR_INVALID_ARG, "%s: negative size (B=%lld T=%lld num_free=%lld)", fn, (long long)a.B,
+                    (long long)a.T, (long long)a.num_free);
+    if (a.B > kMaxRequests)
+        return fail(MNB_ERR_UNSUPPORTED, "%s: B=%lld above %lld", fn, (long long)a.B, (long long)kMaxRequests);
+    if (a.page_size < 1 || a.num_pages < 1 || a.page_size > kMaxSlots || a.num_pages > kMaxSlots / a.page_size)
         return fail(MNB_ERR_SHAPE, "%s: %lld pages of %lld tokens (at least one, at most 2^31 - 64 tokens)", fn,
-                    (long long)num_pages, (long long)page_size);
-    if (max_blocks < 1 || max_blocks > kMaxSlots / page_size || table_stride < max_blocks || table_stride > kMaxStride)
-        return fail(MNB_ERR_SHAPE, "%s: block table of %lld columns, row stride %lld", fn, (long long)max_blocks,
-                    (long long)table_stride);
-    if (T > kMaxDim || num_free > kMaxDim)
+                    (long long)a.num_pages, (long long)a.page_size);
+    if (a.max_blocks < 1 || a.max_blocks > kMaxSlots / a.page_size || a.table_stride < a.max_blocks ||
+        a.table_stride > kMaxStride)
+        return fail(MNB_ERR_SHAPE, "%s: block table of %lld columns, row stride %lld", fn, (long long)a.max_blocks,
+                    (long long)a.table_stride);
+    if (a.T > kMaxDim || a.num_free > kMaxDim)
         return fail(MNB_ERR_SHAPE, "%s: T or num_free above 2^30", fn);
     if (flags & ~(unsigned)MNB_FLAG_PDL)
         return fail(MNB_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
-    if ((B > 0 && (!ctx_lens || !new_lens || !block_table || !seq_lens)) || (num_free > 0 && !free_pages) ||
-        (T > 0 && (!slots || !positions)) || !free_start || !free_next || !cu_new)
+    if ((a.B > 0 && (!a.ctx_lens || !a.new_lens || !a.block_table || !a.seq_lens)) ||
+        (a.num_free > 0 && !a.free_pages) || (a.T > 0 && (!a.slots || !a.positions)) || !a.free_start || !a.free_next || !a.cu_new)
         return fail(MNB_ERR_INVALID_ARG, "%s: NULL pointer", fn);
-    for (const void *ptr : {(const void *)ctx_lens, (const void *)new_lens, (const void *)free_pages,
-                            (const void *)free_start, (const void *)block_table, (const void *)seq_lens,
-                            (const void *)cu_new, (const void *)slots, (const void *)positions,
-                            (const void *)free_next, (const void *)status})
+    for (const void *ptr : {(const void *)a.ctx_lens, (const void *)a.new_lens, (const void *)a.free_pages,
+                            (const void *)a.free_start, (const void *)a.block_table, (const void *)a.seq_lens,
+                            (const void *)a.cu_new, (const void *)a.slots, (const void *)a.positions,
+                            (const void *)a.free_next, (const void *)a.status})
         if (!aligned(ptr, 4))
             return fail(MNB_ERR_ALIGN, "%s: a pointer is not 4-byte aligned", fn);
-    if (free_next == free_start || (B > 0 && (seq_lens == ctx_lens || seq_lens == new_lens)))
+    if (a.free_next == a.free_start || (a.B > 0 && (a.seq_lens == a.ctx_lens || a.seq_lens == a.new_lens)))
         return fail(MNB_ERR_INVALID_ARG, "%s: an output is an input's buffer", fn);
-    return launch_paged_tables(ctx_lens, new_lens, (int)B, (int)page_size, (int)num_pages, free_pages, (int)num_free,
-                               free_start, block_table, table_stride, (int)max_blocks, seq_lens, cu_new, slots,
-                               positions, (int)T, free_next, status, flags, (cudaStream_t)stream);
+    return launch_paged_tables(a.ctx_lens, a.new_lens, (int)a.B, (int)a.page_size, (int)a.num_pages, a.free_pages,
+                               (int)a.num_free, a.free_start, a.block_table, a.table_stride, (int)a.max_blocks,
+                               a.seq_lens, a.cu_new, a.slots, a.positions, (int)a.T, a.free_next, a.status, flags,
+                               (cudaStream_t)stream);
 }
 
-int mnb_rope_append(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs,
-                    const void *v, int64_t v_ts, int64_t v_hs, const mnb_paged_cache *given, const int32_t *slots,
-                    const int32_t *positions, int64_t T, int64_t Hq, const float *cos, const float *sin,
-                    int64_t rot_dim, int64_t num_pos, const float *q_weight, const float *k_weight, float eps,
-                    void *q_out, int64_t o_ts, int64_t o_hs, int *status, unsigned flags, void *stream) {
+int mnb_rope_append(const mnb_rope_append_args *args, unsigned flags, void *stream) {
     clear_error();
     const char *fn = "mnb_rope_append";
+    if (!args)
+        return fail(MNB_ERR_INVALID_ARG, "%s: NULL arguments", fn);
     mnb_paged_cache pool, *cache = &pool;
-    int rc = check_paged_cache(fn, given, cache);
+    int rc = check_paged_cache(fn, &args->cache, cache);
+    const void *q = args->q, *k = args->k, *v = args->v;
+    void *q_out = args->q_out;
+    const int32_t *slots = args->slots, *positions = args->positions;
+    const float *cos = args->cos, *sin = args->sin, *q_weight = args->q_weight, *k_weight = args->k_weight;
+    int *status = args->status;
+    int64_t q_ts = args->q_token_stride, q_hs = args->q_head_stride, k_ts = args->k_token_stride;
+    int64_t k_hs = args->k_head_stride, v_ts = args->v_token_stride, v_hs = args->v_head_stride;
+    int64_t o_ts = args->o_token_stride, o_hs = args->o_head_stride;
+    const int64_t T = args->T, Hq = args->Hq, rot_dim = args->rot_dim, num_pos = args->num_pos;
+    const float eps = args->eps;
     if (rc)
         return rc;
     if (T < 0 || Hq < 0 || rot_dim < 0)
@@ -612,14 +619,23 @@ size_t mnb_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, i
     return paged_attention_workspace_bytes((int)Hq, (int)Hkv, (int)D, dtype == MNB_F16);
 }
 
-int mnb_paged_attention(const void *q, int64_t q_bs, int64_t q_hs, const mnb_paged_cache *given,
-                        const int32_t *block_table, int64_t table_stride, int64_t max_blocks, const int32_t *seq_lens,
-                        int64_t B, int64_t Hq, float scale, void *out, int64_t o_bs, int64_t o_hs, float *lse,
-                        void *workspace, size_t ws_bytes, int *status, unsigned flags, void *stream) {
+int mnb_paged_attention(const mnb_paged_attention_args *args, unsigned flags, void *stream) {
     clear_error();
     const char *fn = "mnb_paged_attention";
+    if (!args)
+        return fail(MNB_ERR_INVALID_ARG, "%s: NULL arguments", fn);
     mnb_paged_cache pool, *cache = &pool;
-    int rc = check_paged_cache(fn, given, cache);
+    int rc = check_paged_cache(fn, &args->cache, cache);
+    const void *q = args->q;
+    void *out = args->out, *workspace = args->workspace;
+    float *lse = args->lse;
+    const int32_t *block_table = args->block_table, *seq_lens = args->seq_lens;
+    int *status = args->status;
+    int64_t q_bs = args->q_request_stride, q_hs = args->q_head_stride, o_bs = args->o_request_stride;
+    int64_t o_hs = args->o_head_stride;
+    const int64_t table_stride = args->table_stride, max_blocks = args->max_blocks, B = args->B, Hq = args->Hq;
+    const size_t ws_bytes = args->ws_bytes;
+    const float scale = args->scale;
     if (rc)
         return rc;
     if (B < 0 || Hq < 1)

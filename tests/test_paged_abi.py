@@ -1,7 +1,5 @@
 """Refusals of the paged cache's entry points, without a GPU: the C ABI with addresses that are never used, and the
 binding's checks of tensors."""
-import ctypes
-
 import pytest
 import torch
 
@@ -17,11 +15,21 @@ def mnb():
     return m
 
 
-def cache(mnb, **kw):
-    d = dict(k=A, v=A, num_pages=10, page_size=16, num_heads=8, head_dim=128, page_stride=16 * 8 * 128,
+CACHE = dict(k=A, v=A, num_pages=10, page_size=16, num_heads=8, head_dim=128, page_stride=16 * 8 * 128,
              slot_stride=8 * 128, head_stride=128, dtype=F16, reserved=0)
-    d.update(kw)
-    return mnb.mnb_paged_cache(*[d[n] for n, _ in mnb.mnb_paged_cache._fields_])
+
+
+def cache(**kw):
+    assert set(kw) <= set(CACHE)
+    return [0 if v is None else v for v in {**CACHE, **kw}.values()]
+
+
+def call(fn, pack, fields, kw, flags):
+    assert set(kw) <= set(fields)
+    vals = []
+    for v in {**fields, **kw}.values():
+        vals += v if isinstance(v, list) else [0 if v is None else v]
+    return fn(pack(*vals), flags, None)
 
 
 BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(dtype=2), INVALID), (dict(num_pages=0), SHAPE),
@@ -32,12 +40,10 @@ BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(dtype=2), 
               (dict(dtype=F32, head_stride=130), ALIGN)]
 
 
-def tables(mnb, **kw):
-    d = dict(ctx=A, new=A + 64, B=4, page=16, pages=10, free=A, nfree=10, start=A, table=A, stride=8, blocks=8,
-             seq=A + 128, cu=A, slots=A, pos=A, T=4, next=A + 4, status=None, flags=0, stream=None)
-    assert set(kw) <= set(d)
-    d.update(kw)
-    return mnb._lib.mnb_paged_tables(*d.values())
+def tables(mnb, flags=0, **kw):
+    d = dict(ctx=A, new=A + 64, free=A, start=A, table=A, seq=A + 128, cu=A, slots=A, pos=A, next=A + 4, status=None,
+             B=4, T=4, page=16, pages=10, nfree=10, stride=8, blocks=8)
+    return call(mnb._lib.mnb_paged_tables, mnb._pack_tables, d, kw, flags)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -53,14 +59,11 @@ def test_tables_refusals(mnb, kw, rc):
     assert "mnb_paged_tables" in mnb.mnb_last_error()
 
 
-def append(mnb, c=None, **kw):
-    d = dict(q=A, qt=4096, qh=128, k=A, kt=4096, kh=128, v=A, vt=4096, vh=128, cache=c or cache(mnb), slots=A, pos=A,
-             T=4, Hq=16, cos=A, sin=A, R=128, num_pos=100, qw=A, kw=A, eps=1e-6, o=A + 4096, ot=2048, oh=128,
-             status=None, flags=0, stream=None)
-    assert set(kw) <= set(d)
-    d.update(kw)
-    d["cache"] = ctypes.byref(d["cache"]) if d["cache"] is not None else None
-    return mnb._lib.mnb_rope_append(*d.values())
+def append(mnb, c=None, flags=0, **kw):
+    d = dict(q=A, k=A, v=A, o=A + 4096, slots=A, pos=A, cos=A, sin=A, qw=A, kw=A, status=None, cache=c or cache(),
+             qt=4096, qh=128, kt=4096, kh=128, vt=4096, vh=128, ot=2048, oh=128, T=4, Hq=16, R=128, num_pos=100,
+             eps=1e-6, reserved=0)
+    return call(mnb._lib.mnb_rope_append, mnb._pack_append, d, kw, flags)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -78,17 +81,14 @@ def test_append_refusals(mnb, kw, rc):
 
 def test_append_refuses_rows_on_one_another(mnb):
     for kw in (dict(head_stride=64), dict(slot_stride=0), dict(page_stride=120)):
-        assert append(mnb, cache(mnb, **kw)) == SHAPE
+        assert append(mnb, cache(**kw)) == SHAPE
     assert append(mnb, T=0) == OK
 
 
-def attention(mnb, c=None, **kw):
-    d = dict(q=A, qb=2048, qh=128, cache=c or cache(mnb), table=A, stride=8, blocks=8, lens=A, B=4, Hq=16, scale=0.1,
-             out=A, ob=2048, oh=128, lse=None, ws=A, nws=1 << 30, status=None, flags=0, stream=None)
-    assert set(kw) <= set(d)
-    d.update(kw)
-    d["cache"] = ctypes.byref(d["cache"]) if d["cache"] is not None else None
-    return mnb._lib.mnb_paged_attention(*d.values())
+def attention(mnb, c=None, flags=0, **kw):
+    d = dict(q=A, out=A, lse=None, table=A, lens=A, ws=A, status=None, cache=c or cache(), qb=2048, qh=128, ob=2048,
+             oh=128, stride=8, blocks=8, B=4, Hq=16, nws=1 << 30, scale=0.1, reserved=0)
+    return call(mnb._lib.mnb_paged_attention, mnb._pack_attention, d, kw, flags)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -106,14 +106,35 @@ def test_attention_refusals(mnb, kw, rc):
 
 @pytest.mark.parametrize("kw,rc", BAD_CACHES)
 def test_cache_refusals(mnb, kw, rc):
-    assert append(mnb, cache(mnb, **kw)) == rc
-    assert attention(mnb, cache(mnb, **kw)) == rc
+    assert append(mnb, cache(**kw)) == rc
+    assert attention(mnb, cache(**kw)) == rc
 
 
 def test_nothing_to_do(mnb):
     assert attention(mnb, B=0) == OK
-    assert mnb._lib.mnb_rope_append(*[None, 0, 0] * 3, None, *[None] * 2, 0, 0, None, None, 0, 0, None, None, 0.0,
-                                    None, 0, 0, None, 0, None) == INVALID      # no cache
+    for fn in (mnb._lib.mnb_paged_tables, mnb._lib.mnb_rope_append, mnb._lib.mnb_paged_attention):
+        assert fn(None, 0, None) == INVALID      # no arguments
+
+
+def test_packed_arguments_have_the_structs_layout(tmp_path):
+    """Sizes and a late offset of the argument structs, as a C compiler lays them out, against the packing."""
+    import os
+    import struct
+    import subprocess
+
+    import int4_block_quantized_matmulnbits_b200 as m
+
+    src = tmp_path / "s.c"
+    src.write_text('#include <stdio.h>\n#include "mnb.h"\nint main(void) { printf("%zu %zu %zu %zu %zu %zu\\n", '
+                   "sizeof(mnb_paged_tables_args), sizeof(mnb_rope_append_args), sizeof(mnb_paged_attention_args), "
+                   "offsetof(mnb_paged_tables_args, B), offsetof(mnb_rope_append_args, q_token_stride), "
+                   "offsetof(mnb_paged_attention_args, scale)); return 0; }")
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.check_call(["gcc", "-I", inc, str(src), "-o", str(tmp_path / "s")])
+    got = [int(x) for x in subprocess.check_output([str(tmp_path / "s")]).split()]
+    c = m._CACHE
+    assert got == [struct.calcsize("@" + f) for f in ("11P7q", "11P" + c + "12qfi", "7P" + c + "8qNfi", "11P", "11P" + c,
+                                                      "7P" + c + "8qN")]
 
 
 def test_workspace_bytes(mnb):
