@@ -49,21 +49,22 @@ struct AttnParams {
     int64_t q_bs, q_hs, o_bs, o_hs;                             // elements
     int64_t table_stride, page_stride, slot_stride, head_stride;
     int G, Hkv, D, rows, row_tiles, page, num_pages, cap;       // cap: rows the table has room for
-    int one_page, whole;   // a tile's keys are in one page: page % TK == 0; and D == DP
+    int one_page;          // a tile's keys are in one page: page % TK == 0
     int split, groups, stages;
     Div by_page, by_split, by_groups;
     float scale;
 };
 
-// Element type, padded head size, rows of query heads per segment.  A tile is
+// Element type, padded head size and whether D fills it, rows of query heads per segment.  A tile is
 // 8 KB of K and V (16 KB for heads of 256): 16 keys of 128 fp16 entries.
 // Rows are swizzled in shared memory (chunk ^ row % 8), so that reads of eight
 // rows' same chunk meet no bank twice.
-template <typename T_, int DP_, int ROWS_>
+template <typename T_, int DP_, int ROWS_, bool WHOLE_>
 struct Cfg {
     using T = T_;
     static constexpr bool F16 = std::is_same<T, half>::value;
     static constexpr int DP = DP_, ROWS = ROWS_;
+    static constexpr bool WHOLE = WHOLE_;                            // D == DP
     static constexpr int TK = (F16 ? 16 : 8) * (DP <= 64 ? 2 : 1);   // keys per tile
     static constexpr int NCH = DP * (int)sizeof(T) / 16;             // 16-byte chunks per row
     static constexpr int ROW_BYTES = DP * (int)sizeof(T);
@@ -177,14 +178,16 @@ struct Acc<C, true> {
     }
 
     // One tile: K and V in shared memory, `valid` one bit per key.
-    __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t, int, uint32_t valid, float scale2) {
+    __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t, int, int D, uint32_t valid, float scale2) {
         const int lane = threadIdx.x & 31, g = lane >> 2;
         float s[KB][NT][4];
         {
             float h[2][KB][NT][4] = {};   // even and odd steps: two chains of products
             const int kr = (lane & 7) + ((lane >> 3) & 1) * 8, kc = lane >> 4;
 #pragma unroll
-            for (int kk = 0; kk < KS; kk++)
+            for (int kk = 0; kk < KS; kk++) {
+                if (!C::WHOLE && kk * 16 >= D)
+                    break;
 #pragma unroll
                 for (int b = 0; b < KB; b++) {
                     uint32_t a0, a1, a2, a3;
@@ -193,6 +196,7 @@ struct Acc<C, true> {
                     for (int t = 0; t < NT; t++)
                         mma16816(h[kk & 1][b][t], a0, a1, a2, a3, q[kk][t][0], q[kk][t][1]);
                 }
+            }
 #pragma unroll
             for (int b = 0; b < KB; b++)
 #pragma unroll
@@ -249,7 +253,9 @@ struct Acc<C, true> {
         }
         const int vr = (lane & 7) + (lane >> 4) * 8, vc = (lane >> 3) & 1;
 #pragma unroll
-        for (int k = 0; k < KS; k++)
+        for (int k = 0; k < KS; k++) {
+            if (!C::WHOLE && k * 16 >= D)
+                break;
 #pragma unroll
             for (int b = 0; b < KB; b++) {
                 uint32_t a0, a1, a2, a3;
@@ -258,6 +264,7 @@ struct Acc<C, true> {
                 for (int t = 0; t < NT; t++)
                     mma16816(o[k][t], a0, a1, a2, a3, p[b][t][0], p[b][t][1]);
             }
+        }
     }
 
     // Sums over the lanes' keys.
@@ -303,10 +310,20 @@ struct Acc<C, false> {
     static constexpr int PER = C::NCH / LPR;                // chunks a lane holds
     static constexpr int KSPLIT = 32 / LPR;                 // keys taken at a time
     static constexpr float kSumScale = 1.0f;
+    static constexpr int QC = C::NCH / 4;                   // chunks of a query row that a lane needs
+    static constexpr bool QREG = C::ROWS * QC <= 16;        // they stay in registers
     float4 o[C::ROWS][PER];
+    float4 q[QREG ? C::ROWS : 1][QREG ? QC : 1];
     float m[C::ROWS], l[C::ROWS];
 
-    __device__ __forceinline__ void open(uint32_t, int) {
+    __device__ __forceinline__ void open(uint32_t qs, int rows) {
+        const int quarter = (threadIdx.x & 31) >> 3;
+        if constexpr (QREG)
+#pragma unroll
+            for (int r = 0; r < C::ROWS; r++)
+#pragma unroll
+                for (int c = 0; c < QC; c++)
+                    q[r][c] = lds4(qs + C::at(min(r, rows - 1), c * 4 + quarter));
 #pragma unroll
         for (int r = 0; r < C::ROWS; r++) {
 #pragma unroll
@@ -317,24 +334,26 @@ struct Acc<C, false> {
         }
     }
 
-    __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t qs, int rows, uint32_t valid, float scale2) {
+    __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t qs, int rows, int D, uint32_t valid, float scale2) {
 #pragma unroll 1
         for (int j = 0; j < C::TK / 8; j++)
-            eight(ks + j * 8 * C::ROW_BYTES, vs + j * 8 * C::ROW_BYTES, qs, rows, valid >> (8 * j), scale2);
+            eight(ks + j * 8 * C::ROW_BYTES, vs + j * 8 * C::ROW_BYTES, qs, rows, D, valid >> (8 * j), scale2);
     }
 
-    __device__ __forceinline__ void eight(uint32_t ks, uint32_t vs, uint32_t qs, int rows, uint32_t valid, float scale2) {
+    __device__ __forceinline__ void eight(uint32_t ks, uint32_t vs, uint32_t qs, int rows, int D, uint32_t valid, float scale2) {
         const int lane = threadIdx.x & 31, key = lane & 7, quarter = lane >> 3;
         float s[C::ROWS] = {};
-#pragma unroll 4
-        for (int c = 0; c < C::NCH / 4; c++) {
+#pragma unroll(QREG ? QC : 4)
+        for (int c = 0; c < QC; c++) {
+            if (!C::WHOLE && c * 16 >= D)
+                break;
             const int ch = c * 4 + quarter;
-            const float4 k = lds4(ks + C::at(key, ch));
+            float4 k = lds4(ks + C::at(key, ch));
+            if (!C::WHOLE && ch * 4 >= D)   // columns that nothing has written
+                k = make_float4(0, 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < C::ROWS; r++) {
-                const int qr = min(r, rows - 1);
-                s[r] = dot(k, lds4(qs + C::at(qr, ch)), s[r]);
-            }
+            for (int r = 0; r < C::ROWS; r++)
+                s[r] = dot(k, QREG ? q[QREG ? r : 0][QREG ? c : 0] : lds4(qs + C::at(min(r, rows - 1), ch)), s[r]);
         }
         const bool ok = (valid >> key) & 1;
         bool over = false;
@@ -462,7 +481,7 @@ struct Feed {
             valid = __ballot_sync(0xffffffffu, has) & want;
         if (valid != want && p.status)
             atomicOr(p.status, 1);
-        if (p.whole && valid == kAll) {   // one page, every key, every column
+        if (p.one_page && valid == kAll) {   // one page, every key: the rows are slot_stride apart
             const T *k = (const T *)p.k + off + sub * p.slot_stride + ch0 * EPC;
             const T *v = (const T *)p.v + off + sub * p.slot_stride + ch0 * EPC;
             const int64_t step = RPI * p.slot_stride;
@@ -470,10 +489,11 @@ struct Feed {
             for (int j = 0; j < C::TK / RPI; j++) {
                 const uint32_t d = dst + j * RPI * C::ROW_BYTES + (sw ^ ((j * RPI & 7) << 4));
 #pragma unroll
-                for (int c = 0; c < CPL; c++) {
-                    cp_async16(d + c * 512, k + c * 32 * EPC);
-                    cp_async16(d + c * 512 + C::TILE_BYTES, v + c * 32 * EPC);
-                }
+                for (int c = 0; c < CPL; c++)
+                    if (C::WHOLE || (ch0 + c * 32) * EPC < p.D) {
+                        cp_async16(d + c * 512, k + c * 32 * EPC);
+                        cp_async16(d + c * 512 + C::TILE_BYTES, v + c * 32 * EPC);
+                    }
                 k += step, v += step;
             }
             return valid;
@@ -484,13 +504,14 @@ struct Feed {
             const int64_t ro = (p.one_page ? off + row * p.slot_stride : __shfl_sync(0xffffffffu, off, row)) + ch0 * EPC;
             const bool ok = (valid >> row) & 1;
             const uint32_t d = dst + j * RPI * C::ROW_BYTES + (sw ^ ((j * RPI & 7) << 4));
+            const T *k = (const T *)p.k + (ok ? ro : 0), *v = (const T *)p.v + (ok ? ro : 0);
+            const int n = ok ? 16 : 0;
 #pragma unroll
-            for (int c = 0; c < CPL; c++) {
-                const bool in = ok && (ch0 + c * 32) * EPC < p.D;
-                const int64_t at = in ? ro + c * 32 * EPC : 0;
-                cp_async16(d + c * 512, (const T *)p.k + at, in ? 16 : 0);
-                cp_async16(d + c * 512 + C::TILE_BYTES, (const T *)p.v + at, in ? 16 : 0);
-            }
+            for (int c = 0; c < CPL; c++)
+                if (C::WHOLE || (ch0 + c * 32) * EPC < p.D) {
+                    cp_async16(d + c * 512, k + c * 32 * EPC, n);
+                    cp_async16(d + c * 512 + C::TILE_BYTES, v + c * 32 * EPC, n);
+                }
         }
         return valid;
     }
@@ -585,6 +606,12 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
     const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, r0 = (seg - h * p.row_tiles) * C::ROWS;
     auto head_of = [&](int r) { return r0 + r < p.G ? h * p.G + r0 + r : -1; };   // of row r of the segment
 
+    // half a step of 16 entries is beyond D: K's there, which no copy writes, must be finite
+    if (C::F16 && !C::WHOLE && p.D % 16)
+        for (int i = lane; i < p.stages * C::TK; i += 32)
+            *reinterpret_cast<uint4 *>(my_ring + i / C::TK * 2 * C::TILE_BYTES + C::at(i % C::TK, p.D / 8)) =
+                make_uint4(0, 0, 0, 0);
+
     pdl_wait();
     pdl_launch_dependents();
     const int given = p.lens[b], len = min(max(given, 0), p.cap);
@@ -641,7 +668,7 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
             cp_wait_rt(p.stages - 1);
             __syncwarp();
             const uint32_t ks = ring + stage * 2 * C::TILE_BYTES;
-            acc.tile(ks, ks + C::TILE_BYTES, qs, p.rows, vmask[warp][stage], p.scale * kLog2e);
+            acc.tile(ks, ks + C::TILE_BYTES, qs, p.rows, p.D, vmask[warp][stage], p.scale * kLog2e);
             stage = stage + 1 == p.stages ? 0 : stage + 1;
         }
         acc.finish();
@@ -762,28 +789,41 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
     const int64_t all = (int64_t)B * segs;
     const int tiles = (p.cap - 1) / C::TK + 1;   // of the longest request that the table has room for
     p.one_page = p.page % C::TK == 0;
-    p.whole = p.one_page && p.D == C::DP;
-    // An SM has room for kWarpsMost warps' rings: as one CTA while a cluster of 8 of
-    // them per segment can run at once, else as two or three CTAs.
-    const int ctas_sm = all <= clusters_at_once(sms, 1, 8) ? 1 : all <= clusters_at_once(sms, 2, 8) ? 2 : 3;
-    int warps = C::kWarpsMost / ctas_sm;
-    int64_t split = kMaxSplit;
-    while (split > 1 && all > clusters_at_once(sms, ctas_sm, (int)split))
-        split--;
-    if (ctas_sm == 3) {   // more CTAs only for work: 4 tiles a warp or more, and not far beyond 32
-        const int64_t most = (tiles - 1) / (warps * 4) + 1, least = (tiles - 1) / (warps * 32) + 1;
-        split = split < most ? split : most;
-        split = split > least ? split : least;
+    // The shape: an SM has room for kWarpsMost warps' rings.  Of the shapes whose CTAs
+    // all run at once, the one with the most warps; of those, where a warp's ring is
+    // 16 KB, the one with the most CTAs, as shorter CTAs even out ragged lengths (16
+    // requests of up to 16384: 97 us as 4 x 3 against 101 us as 1 x 12).  More CTAs
+    // than 1.5 per SM only for work: 4 tiles a warp (16 requests of 128 tokens in 8
+    // heads: 5.4 us as 1 x 4, 9.8 as 4 x 4).
+    const int most = C::kWarpsMost;
+    int split = 1, warps = 0;
+    for (int S = 1; S <= kMaxSplit && S <= tiles; S++) {
+        int k = 1;
+        while (k <= 6 && all > clusters_at_once(sms, k, S))
+            k++;
+        const int W = most / k;
+        if (k > 6 || W < 1 || (S > 1 && 2 * all * S > 3 * sms && (int64_t)4 * S * W > tiles))
+            continue;
+        if (S * W > split * warps || (S * W == split * warps && most == kMaxWarps && W >= 3))
+            split = S, warps = W;
     }
-    split = split < kMaxSplit ? split : kMaxSplit;
-    split = split < tiles ? split : tiles;
+    // More segments than that, or long work for each warp: CTAs of a third of an SM,
+    // about 32 tiles a warp, in turn (64 requests of up to 8192: 167 us as 4 x 4,
+    // 179 as 1 x 4); short segments as CTAs of two warps (256 requests of 100: 27.8
+    // us as 1 x 2, 32 as 1 x 4).
+    if (warps == 0 || (split < kMaxSplit && tiles > 32 * split * warps) || (warps < 3 && tiles > 24 * warps)) {
+        const int W = tiles <= 48 ? 2 : most == kMaxWarps ? 4 : 3, long_split = (tiles - 1) / (32 * W) + 1;
+        split = long_split > split ? long_split : split;
+        split = split < kMaxSplit ? split : kMaxSplit;
+        warps = W;
+    }
     split = g_split ? g_split : split;
-    warps = (tiles - 1) / (int)split + 1 < warps ? (tiles - 1) / (int)split + 1 : warps;
+    warps = (tiles - 1) / split + 1 < warps ? (tiles - 1) / split + 1 : warps;
     warps = g_warps ? g_warps < C::kWarpsMost ? g_warps : C::kWarpsMost : warps;
     // Groups: where the clusters of a few long segments would leave SMs idle, until a warp has 4 tiles.
     int64_t groups = 1;
-    if (ctas_sm == 1 && tiles > 6 * split * warps) {
-        const int64_t want = (tiles - 1) / (4 * split * warps) + 1, room = clusters_at_once(sms, 1, (int)split) / all;
+    if (all <= clusters_at_once(sms, 1, kMaxSplit) && tiles > 6 * split * warps) {
+        const int64_t want = (tiles - 1) / (4 * split * warps) + 1, room = clusters_at_once(sms, 1, split) / all;
         groups = want < room ? want : room;
     }
     groups = g_groups ? g_groups : groups;
@@ -792,13 +832,13 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
     // A deeper ring where the CTAs leave room for one.
     const size_t stage = (size_t)warps * 2 * C::TILE_BYTES, q_bytes = (size_t)p.rows * C::ROW_BYTES;
     int per_sm = 1;
-    while (per_sm < C::kWarpsMost / warps && all * groups > clusters_at_once(sms, per_sm, (int)split))
+    while (per_sm < C::kWarpsMost / warps && all * groups > clusters_at_once(sms, per_sm, split))
         per_sm++;
     size_t room = kSmemSm / per_sm - 1024 - 512;
     room = room < kSmemMax ? room : kSmemMax;
     const size_t fit = (room - q_bytes) / stage;
     p.stages = fit < 2 ? 2 : fit > kMaxStages ? kMaxStages : (int)fit;
-    p.split = (int)split, p.groups = (int)groups;
+    p.split = split, p.groups = (int)groups;
     p.by_page = div_by((uint32_t)p.page), p.by_split = div_by((uint32_t)split), p.by_groups = div_by((uint32_t)groups);
 
     cudaLaunchConfig_t cfg = {};
@@ -829,7 +869,7 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
 
 template <typename T, int DP, int ROWS>
 int launch_rows(const AttnParams &p, int B, unsigned flags, cudaStream_t s) {
-    return launch_cfg<Cfg<T, DP, ROWS>>(p, B, flags, s);
+    return p.D == DP ? launch_cfg<Cfg<T, DP, ROWS, true>>(p, B, flags, s) : launch_cfg<Cfg<T, DP, ROWS, false>>(p, B, flags, s);
 }
 
 template <typename T, int DP>

@@ -251,6 +251,9 @@ CASES = [
     ([9000], 8, 8, 64, 16, False),           # cut over all SMs
     ([9000, 1, 0, 4500], 5, 1, 40, 16, True),
     (list(range(0, 300)), 2, 2, 64, 16, False),
+    ([333, 17, 250], 6, 2, 200, 16, True),
+    ([333, 17, 250], 3, 1, 72, 48, False),
+    ([100, 9], 10, 1, 24, 5, False),
     ([64] * 97, 4, 2, 128, 16, False),
 ]
 
