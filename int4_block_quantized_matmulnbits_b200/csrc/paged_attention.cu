@@ -51,6 +51,7 @@ struct AttnParams {
     int G, Hkv, D, rows, row_tiles, page, num_pages, cap;       // cap: rows the table has room for
     int one_page;          // a tile's keys are in one page: page % TK == 0
     int split, groups, stages;
+    int least;             // fewest tiles that a CTA of a cluster takes
     Div by_page, by_split, by_groups;
     float scale;
 };
@@ -624,7 +625,11 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
     if (group > 0 && g0 >= tiles)
         return;
     const int used_groups = P == 1 || tiles == 0 ? 1 : (tiles + per_group - 1) / per_group;
-    const int per = S == 1 ? g1 - g0 : quotient(g1 - g0 + S - 1, p.by_split);
+    // a segment too short for all S CTAs leaves the last of them idle; one for a single CTA needs no cluster
+    const int per = S == 1 ? g1 - g0 : max(quotient(g1 - g0 + S - 1, p.by_split), p.least);
+    const bool joined = per < g1 - g0;
+    if (!joined && rank > 0)
+        return;
     const int t0 = g0 + rank * per, t1 = min(g1, t0 + per);
 
     const int32_t *row = p.table + b * p.table_stride;
@@ -714,7 +719,7 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
             const float4 o = merge(parts, lane < parts ? ml[0] : -INFINITY, lane < parts ? ml[p.rows] : 0.0f, M, L, [&](int i) {
                 return *reinterpret_cast<const float4 *>(smem + (size_t)i * kRing + (r * p.D + (c < p.D ? c : 0)) * 4);
             });
-            if (S > 1)
+            if (joined)
                 keep(cta_part, r, c, o, M, L);
             else if (used_groups > 1)
                 keep(group_part, r, c, o, M, L);
@@ -723,9 +728,9 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
         }
     }
     // of the cluster's CTAs
-    if (S > 1) {
+    if (joined) {
         cluster_sync();
-        const int parts = per > 0 ? (g1 - g0 + per - 1) / per : 0;   // CTAs with a tile
+        const int parts = (g1 - g0 + per - 1) / per;   // CTAs with a tile
         const uint32_t at = smem_u32(cta_part);
         for (int task = warp * S + rank; task < tasks; task += W * S) {
             const int r = row_of(task), c = col_of(task);
@@ -838,6 +843,8 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
     room = room < kSmemMax ? room : kSmemMax;
     const size_t fit = (room - q_bytes) / stage;
     p.stages = fit < 2 ? 2 : fit > kMaxStages ? kMaxStages : (int)fit;
+    // few CTAs: every one for the shortest way; many: none for less than two tiles a warp
+    p.least = all * split <= 2 * sms ? 1 : 2 * warps;
     p.split = split, p.groups = (int)groups;
     p.by_page = div_by((uint32_t)p.page), p.by_split = div_by((uint32_t)split), p.by_groups = div_by((uint32_t)groups);
 
