@@ -187,7 +187,7 @@ struct AppendParams {
     int Hq, Hkv, D, R, page, num_pos, num_slots;
     int lph, gpt, tpc;   // lanes a head, groups a token, tokens a CTA
     float eps, inv_D;
-    Div by_page;
+    Div by_page, by_gpt;
 };
 
 // V neighbouring entries in fp32 (V = 4, or 8 of fp16: 16-byte accesses but for 4 of fp16).
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kAppendThreads, V == 8 ? 4 : 6) rope_append_ke
     pdl_launch_dependents();
     const int l = threadIdx.x & (p.lph - 1), group = threadIdx.x / p.lph;
     const unsigned mask = (p.lph == 32 ? 0xffffffffu : (1u << p.lph) - 1) << (threadIdx.x & 31 & ~(p.lph - 1));
-    const int tok = group / p.gpt, h0 = group - tok * p.gpt;
+    const int tok = quotient(group, p.by_gpt), h0 = group - tok * p.gpt;
     const int64_t t = (int64_t)blockIdx.x * p.tpc + tok;
     if (tok >= p.tpc || t >= p.T)
         return;
@@ -362,8 +362,12 @@ int launch_append(AppendParams p, unsigned flags, cudaStream_t s) {
     while (p.lph < units)
         p.lph *= 2;
     const int groups = kAppendThreads / p.lph;
-    const int rounds = (heads + groups - 1) / groups;
+    // With tokens for every SM a group takes two heads of 16-byte pairs, or three of
+    // 8-byte (fp16) or fp32 ones: what the lanes work out per token is then shared
+    // (1024 fp16 tokens: 7.0 us, 7.9 with one head; 8191 fp32 tokens: 27.8 us, 29.9).
+    const int rounds = max((heads + groups - 1) / groups, p.T < 2 * device_sm_count() ? 1 : V == 8 ? 2 : 3);
     p.gpt = (heads + rounds - 1) / rounds;   // as many heads a group for all groups, or one fewer
+    p.by_gpt = div_by((uint32_t)p.gpt);
     p.tpc = groups / p.gpt;
     if (p.T < p.tpc)
         p.tpc = (int)p.T;
