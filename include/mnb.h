@@ -484,7 +484,10 @@ typedef struct mnb_paged_attention_args {
  * the block table and rows of its last page there may hold anything.
  *   lse fp32 [B][Hq] or NULL.  1 <= Hq <= 4096, Hq % Hkv == 0, 0 <= B <= 4096,
  *   max_blocks * page_size <= 2^31 - 64.
- *   Results are the same, bit for bit, from call to call on one GPU model.
+ *   Calls of the same sizes on one GPU model give the same results, bit for bit.
+ *   The launch shape follows B, the heads and max_blocks (the lengths are on the
+ *   device): a table much wider than the longest request needs costs time; a
+ *   view of its first columns serves as well.
  * workspace: mnb_paged_attention_workspace_bytes (for the current device),
  * 16-byte aligned, ZERO-FILLED before its first use; its first bytes count
  * arrivals and every call leaves them zero again, so it serves call after call,
