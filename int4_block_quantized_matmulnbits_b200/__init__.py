@@ -1,6 +1,6 @@
 """MatMulNBits (weight-only int4, block-quantized) for NVIDIA B200 -- Python binding.
 
-A thin ctypes layer over ``libmnb.so`` (the sm_100a kernels and their C ABI,
+A thin layer (ctypes, and ``_binding.so`` for the paged cache's calls) over ``libmnb.so`` (the sm_100a kernels and their C ABI,
 declared in ``include/mnb.h``).  Every function here has the name of the C
 entry point it calls and only marshals arguments: torch tensors become device
 pointers, dtypes become ``mnb_dtype`` values, the stream defaults to torch's
@@ -16,7 +16,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import struct
 
 import torch
 
@@ -115,14 +114,9 @@ def _dt(t):
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-# the current stream's handle without a Stream object around it, where torch offers that
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
 def _stream(stream):
     if stream is None:
-        return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -310,22 +304,19 @@ def mnb_gptq_quantize(W, U, dead, bs, has_zp, packed, scales, zp, stream=None):
 
 
 
-# ---- paged key-value cache.  A decode step makes these calls once per layer, so
-# the checks that pass read each property of a tensor once and call no helper
-# per tensor; what a failed one has found is worked out afterwards, in _explain.
+# ---- paged key-value cache.  A decode step makes these calls once or twice per
+# layer: _binding (csrc/binding.cpp) reads and checks the tensors and makes the C
+# call; what a failed check has found is worked out afterwards, in _explain.
 
-# The C structs of the same names as bytes: one conversion for all fields.
-_CACHE = "PPqqqqqqqii"
-_pack_tables = struct.Struct("@11P7q").pack                            # mnb_paged_tables_args
-_pack_append = struct.Struct("@11P" + _CACHE + "12qfi").pack           # mnb_rope_append_args
-_pack_attention = struct.Struct("@7P" + _CACHE + "8qNfi").pack         # mnb_paged_attention_args
+from . import _binding  # noqa: E402  (built and loaded with libmnb.so)
+
 _PAGED_DT = {torch.float16: MNB_F16, torch.float32: MNB_F32}
 
 
 def _explain(fn, **ts):
     """Raises for the first tensor that is not as described: (tensor, dtype, shape, layout).  layout "flat":
-    contiguous, as many elements as the shape has; "rows": that shape, a contiguous last dimension; "same": the
-    strides of k_cache besides."""
+    contiguous, as many elements as the shape has; "table": contiguous; "rows": a contiguous last dimension; "same":
+    the strides of k_cache besides."""
     for name, (t, dtype, shape, layout) in ts.items():
         if t is None:
             continue
@@ -333,9 +324,9 @@ def _explain(fn, **ts):
             raise MnbError(fn, -1, f"{name} is {t.dtype}, not {dtype}")
         if tuple(t.shape) != shape and (layout != "flat" or t.numel() != math.prod(shape)):
             raise MnbError(fn, -2, f"{name} has shape {tuple(t.shape)}, not {shape}")
-        if layout == "flat" and not t.is_contiguous():
+        if layout in ("flat", "table") and not t.is_contiguous():
             raise MnbError(fn, -1, f"{name} must be contiguous")
-        if layout != "flat" and t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+        if layout in ("rows", "same") and t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
             raise MnbError(fn, -1, f"{name}'s last dimension must be contiguous")
         if layout == "same" and t.stride() != ts["k_cache"][0].stride():
             raise MnbError(fn, -1, f"{name} must have k_cache's strides")
@@ -345,13 +336,12 @@ def _explain(fn, **ts):
     raise MnbError(fn, -1, "arguments do not fit together")
 
 
-def _pool_dtype(fn, k_cache):
-    dt = _PAGED_DT.get(k_cache.dtype)
-    if dt is None:
+def _pool(fn, k_cache):
+    if k_cache.dtype not in _PAGED_DT:
         raise MnbError(fn, -1, f"k_cache is {k_cache.dtype}: fp16 or fp32")
     if k_cache.dim() != 4:
         raise MnbError(fn, -2, f"k_cache has shape {tuple(k_cache.shape)}, not [pages, page_size, heads, head size]")
-    return dt
+    return k_cache.dtype, tuple(k_cache.shape)
 
 
 def mnb_paged_tables(ctx_lens, new_lens, block_table, page_size, num_pages, free_pages, free_start, seq_lens, cu_new,
@@ -359,41 +349,21 @@ def mnb_paged_tables(ctx_lens, new_lens, block_table, page_size, num_pages, free
     """Pages for new_lens [B] more tokens behind ctx_lens [B]: taken from free_pages [F], at free_start [1] and on,
     into block_table [B, blocks]; seq_lens [B], cu_new [B + 1], slots and positions [T] of the new tokens (-1 and 0
     behind the last), free_next [1].  All int32."""
-    fn, i32 = "mnb_paged_tables", torch.int32
-    dev = ctx_lens.get_device()
-    B, T, F = ctx_lens.numel(), slots.numel(), free_pages.numel()
-    rows, blocks = block_table.shape if block_table.dim() == 2 else (-1, -1)
-    stride, last = block_table.stride() if rows >= 0 else (0, 0)
-    if not (dev >= 0 and dev == torch.cuda.current_device() and
-            ctx_lens.dtype is i32 and ctx_lens.is_contiguous() and
-            new_lens.dtype is i32 and new_lens.numel() == B and new_lens.is_contiguous() and
-            new_lens.get_device() == dev and
-            free_pages.dtype is i32 and free_pages.is_contiguous() and free_pages.get_device() == dev and
-            free_start.dtype is i32 and free_start.numel() == 1 and free_start.get_device() == dev and
-            free_next.dtype is i32 and free_next.numel() == 1 and free_next.get_device() == dev and
-            seq_lens.dtype is i32 and seq_lens.numel() == B and seq_lens.is_contiguous() and
-            seq_lens.get_device() == dev and
-            cu_new.dtype is i32 and cu_new.numel() == B + 1 and cu_new.is_contiguous() and
-            cu_new.get_device() == dev and
-            slots.dtype is i32 and slots.is_contiguous() and slots.get_device() == dev and
-            positions.dtype is i32 and positions.numel() == T and positions.is_contiguous() and
-            positions.get_device() == dev and
-            block_table.dtype is i32 and rows == B and (last == 1 or blocks == 1 or B == 0) and
-            block_table.get_device() == dev and
-            (status is None or (status.dtype is i32 and status.numel() == 1 and status.get_device() == dev))):
-        _explain(fn, ctx_lens=(ctx_lens, i32, (B,), "flat"), new_lens=(new_lens, i32, (B,), "flat"),
-                 block_table=(block_table, i32, (B, blocks), "rows"), free_pages=(free_pages, i32, (F,), "flat"),
+    rc = _binding.paged_tables(ctx_lens, new_lens, block_table, page_size, num_pages, free_pages, free_start, seq_lens,
+                               slots, positions, cu_new, free_next, status, flags,
+                               None if stream is None else _stream(stream))
+    if rc is None:
+        i32, B, T = torch.int32, ctx_lens.numel(), slots.numel()
+        _explain("mnb_paged_tables", ctx_lens=(ctx_lens, i32, (B,), "flat"), new_lens=(new_lens, i32, (B,), "flat"),
+                 block_table=(block_table, i32, (B, block_table.shape[-1]), "rows"),
+                 free_pages=(free_pages, i32, (free_pages.numel(),), "flat"),
                  free_start=(free_start, i32, (1,), "flat"), seq_lens=(seq_lens, i32, (B,), "flat"),
                  cu_new=(cu_new, i32, (B + 1,), "flat"), slots=(slots, i32, (T,), "flat"),
                  positions=(positions, i32, (T,), "flat"), free_next=(free_next, i32, (1,), "flat"),
                  status=(status, i32, (1,), "flat"))
-    rc = _lib.mnb_paged_tables(_pack_tables(
-        ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), free_start.data_ptr(),
-        block_table.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-        free_next.data_ptr(), 0 if status is None else status.data_ptr(), B, T, page_size, num_pages, F,
-        stride if B > 1 else blocks, blocks), flags, _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
-        _check(fn, rc)
+        _check("mnb_paged_tables", rc)
+
 
 
 def mnb_rope_append(q, k, v, k_cache, v_cache, slots, positions, cos, sin, q_out, q_weight=None, k_weight=None,
@@ -401,67 +371,25 @@ def mnb_rope_append(q, k, v, k_cache, v_cache, slots, positions, cos, sin, q_out
     """RMS norm (where a weight [D] is given) and rotary embedding (unless cos is None) of q [T, Hq, D] into q_out and
     of k [T, Hkv, D] into rows slots [T] of k_cache [pages, page_size, Hkv, D]; v likewise, as it is, into v_cache.
     cos, sin: fp32 [positions, rot_dim / 2].  q and q_out may be None (keys and values alone), or one tensor."""
-    fn, f32, i32, dtype = "mnb_rope_append", torch.float32, torch.int32, k_cache.dtype
+    fn = "mnb_rope_append"
     if (q is None) != (q_out is None) or (cos is None) != (sin is None) or (cos is not None and positions is None):
         raise MnbError(fn, -1, "q and q_out go together, and cos, sin and positions")
-    dt, dev = _pool_dtype(fn, k_cache), k_cache.get_device()
-    shape, strides = k_cache.shape, k_cache.stride()
-    P, ps, H, D = shape
-    T = slots.numel()
-    rows = (T, H, D)
-    ks = vs = qs = os_ = (0, 0, 1)
-    ok = (dev >= 0 and dev == torch.cuda.current_device() and
-          v_cache.shape == shape and v_cache.dtype is dtype and v_cache.get_device() == dev and
-          v_cache.stride() == strides and (strides[3] == 1 or D == 1) and
-          k.shape == rows and k.dtype is dtype and k.get_device() == dev and
-          v.shape == rows and v.dtype is dtype and v.get_device() == dev and
-          slots.dtype is i32 and slots.is_contiguous() and slots.get_device() == dev and
-          (status is None or (status.dtype is i32 and status.numel() == 1 and status.get_device() == dev)))
-    if ok:
-        ks, vs = k.stride(), v.stride()
-        ok = (ks[2] == 1 and vs[2] == 1) or T * D <= 1
-    Hq = half = num_pos = 0
-    qp = op = cp = sp = pp = qwp = kwp = 0
-    if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else -1
-        rows = (T, Hq, D)
-        ok = (ok and q.shape == rows and q.dtype is dtype and q.get_device() == dev and
-              q_out.shape == rows and q_out.dtype is dtype and q_out.get_device() == dev)
-        if ok:
-            qs, os_ = q.stride(), q_out.stride()
-            ok = (qs[2] == 1 and os_[2] == 1) or T * D <= 1
-        qp, op = q.data_ptr(), q_out.data_ptr()
-    if positions is not None:
-        ok = (ok and positions.dtype is i32 and positions.numel() == T and positions.is_contiguous() and
-              positions.get_device() == dev)
-        pp = positions.data_ptr()
-    if cos is not None:
-        num_pos, half = cos.shape if cos.dim() == 2 else (-1, 0)
-        ok = (ok and cos.dtype is f32 and cos.is_contiguous() and cos.get_device() == dev and num_pos >= 0 and
-              sin.dtype is f32 and sin.shape == cos.shape and sin.is_contiguous() and sin.get_device() == dev)
-        cp, sp = cos.data_ptr(), sin.data_ptr()
-    if q_weight is not None:
-        ok = (ok and q_weight.dtype is f32 and q_weight.numel() == D and q_weight.is_contiguous() and
-              q_weight.get_device() == dev)
-        qwp = q_weight.data_ptr()
-    if k_weight is not None:
-        ok = (ok and k_weight.dtype is f32 and k_weight.numel() == D and k_weight.is_contiguous() and
-              k_weight.get_device() == dev)
-        kwp = k_weight.data_ptr()
-    if not ok:
-        _explain(fn, k_cache=(k_cache, dtype, tuple(shape), "rows"), v_cache=(v_cache, dtype, tuple(shape), "same"),
+    rc = _binding.rope_append(q, k, v, k_cache, v_cache, slots, positions, cos, sin, q_out, q_weight, k_weight, eps,
+                              status, flags, None if stream is None else _stream(stream))
+    if rc is None:
+        (dtype, pool), f32, i32, T = _pool(fn, k_cache), torch.float32, torch.int32, slots.numel()
+        H, D = pool[2:]
+        Hq = q.shape[1] if q is not None and q.dim() == 3 else "Hq"
+        half = tuple(cos.shape) if cos is not None and cos.dim() == 2 else ("positions", "rot_dim / 2")
+        _explain(fn, k_cache=(k_cache, dtype, pool, "rows"), v_cache=(v_cache, dtype, pool, "same"),
                  q=(q, dtype, (T, Hq, D), "rows"), k=(k, dtype, (T, H, D), "rows"), v=(v, dtype, (T, H, D), "rows"),
                  q_out=(q_out, dtype, (T, Hq, D), "rows"), slots=(slots, i32, (T,), "flat"),
-                 positions=(positions, i32, (T,), "flat"), cos=(cos, f32, (num_pos, half), "flat"),
-                 sin=(sin, f32, (num_pos, half), "flat"), q_weight=(q_weight, f32, (D,), "flat"),
+                 positions=(positions, i32, (T,), "flat"), cos=(cos, f32, half, "table"),
+                 sin=(sin, f32, half, "table"), q_weight=(q_weight, f32, (D,), "flat"),
                  k_weight=(k_weight, f32, (D,), "flat"), status=(status, i32, (1,), "flat"))
-    rc = _lib.mnb_rope_append(_pack_append(
-        qp, k.data_ptr(), v.data_ptr(), op, slots.data_ptr(), pp, cp, sp, qwp, kwp,
-        0 if status is None else status.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), P, ps, H, D, strides[0],
-        strides[1], strides[2], dt, 0, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], T, Hq, 2 * half,
-        num_pos, eps, 0), flags, _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(fn, rc)
+
 
 
 def mnb_paged_attention_workspace_bytes(B, Hq, Hkv, D, dtype=torch.float16) -> int:
@@ -474,42 +402,18 @@ def mnb_paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, 
     """out [B, Hq, D] = softmax(scale * q k^T) v of one token per request over the first seq_lens [B] rows of its
     pages block_table [B, blocks] of k_cache, v_cache [pages, page_size, Hkv, D]; lse fp32 [B, Hq].
     workspace: a zero-filled uint8 tensor of mnb_paged_attention_workspace_bytes bytes."""
-    fn, i32, dtype = "mnb_paged_attention", torch.int32, k_cache.dtype
-    dt, dev = _pool_dtype(fn, k_cache), k_cache.get_device()
-    shape, strides = k_cache.shape, k_cache.stride()
-    P, ps, H, D = shape
-    B, Hq, _ = q.shape if q.dim() == 3 else (seq_lens.numel(), -1, D)
-    rows = (B, Hq, D)
-    table_rows, blocks = block_table.shape if block_table.dim() == 2 else (-1, -1)
-    table_stride, last = block_table.stride() if table_rows >= 0 else (0, 0)
-    qs = os_ = (0, 0, 1)
-    ok = (dev >= 0 and dev == torch.cuda.current_device() and
-          v_cache.shape == shape and v_cache.dtype is dtype and v_cache.get_device() == dev and
-          v_cache.stride() == strides and (strides[3] == 1 or D == 1) and
-          q.shape == rows and q.dtype is dtype and q.get_device() == dev and
-          out.shape == rows and out.dtype is dtype and out.get_device() == dev and
-          block_table.dtype is i32 and table_rows == B and (last == 1 or blocks == 1 or B == 0) and
-          block_table.get_device() == dev and
-          seq_lens.dtype is i32 and seq_lens.numel() == B and seq_lens.is_contiguous() and
-          seq_lens.get_device() == dev and
-          workspace.dtype is torch.uint8 and workspace.is_contiguous() and workspace.get_device() == dev and
-          (lse is None or (lse.dtype is torch.float32 and lse.numel() == B * Hq and lse.is_contiguous() and
-                           lse.get_device() == dev)) and
-          (status is None or (status.dtype is i32 and status.numel() == 1 and status.get_device() == dev)))
-    if ok:
-        qs, os_ = q.stride(), out.stride()
-        ok = (qs[2] == 1 and os_[2] == 1) or B * D <= 1
-    if not ok:
-        _explain(fn, k_cache=(k_cache, dtype, tuple(shape), "rows"), v_cache=(v_cache, dtype, tuple(shape), "same"),
+    fn = "mnb_paged_attention"
+    rc = _binding.paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale, out, workspace, lse, status, flags,
+                                  None if stream is None else _stream(stream))
+    if rc is None:
+        (dtype, pool), i32 = _pool(fn, k_cache), torch.int32
+        B, Hq = q.shape[:2] if q.dim() == 3 else (seq_lens.numel(), "Hq")
+        rows = (B, Hq, pool[3])
+        _explain(fn, k_cache=(k_cache, dtype, pool, "rows"), v_cache=(v_cache, dtype, pool, "same"),
                  q=(q, dtype, rows, "rows"), out=(out, dtype, rows, "rows"),
-                 block_table=(block_table, i32, (B, blocks), "rows"), seq_lens=(seq_lens, i32, (B,), "flat"),
+                 block_table=(block_table, i32, (B, block_table.shape[-1]), "rows"),
+                 seq_lens=(seq_lens, i32, (B,), "flat"),
                  workspace=(workspace, torch.uint8, (workspace.numel(),), "flat"),
                  lse=(lse, torch.float32, (B, Hq), "flat"), status=(status, i32, (1,), "flat"))
-    rc = _lib.mnb_paged_attention(_pack_attention(
-        q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(), block_table.data_ptr(),
-        seq_lens.data_ptr(), workspace.data_ptr(), 0 if status is None else status.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), P, ps, H, D, strides[0], strides[1], strides[2], dt, 0, qs[0], qs[1], os_[0], os_[1],
-        table_stride if B > 1 else blocks, blocks, B, Hq, workspace.numel(), scale, 0), flags,
-        _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         _check(fn, rc)

@@ -11,9 +11,11 @@ only needs the NVIDIA driver at run time.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -43,6 +45,27 @@ DEBUG_SOURCES = ["gemv_resident.cu"]
 DEBUG_OUT = os.path.join(HERE, "libmnb_debug.so")
 
 
+BINDING = os.path.join(HERE, "_binding.so")
+
+
+def build_binding(verbose: bool = False) -> str:
+    """_binding.so (csrc/binding.cpp): the paged cache's calls for Python, against torch's headers and libmnb.so."""
+    src, torch = os.path.join(CSRC, "binding.cpp"), os.path.dirname(importlib.util.find_spec("torch").origin)
+    if _stale(BINDING, [src, os.path.join(ROOT, "include", "mnb.h"), os.path.join(torch, "version.py")]):
+        inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+               "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+               "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+               "-I", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), src, "-o", BINDING + ".tmp",
+               "-L", HERE, "-l:libmnb.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+               "-ltorch_python"]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.check_call(cmd)
+        os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, ptxas_verbose: bool = False, debug: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", f) for f in ("mnb.h", "mnb_tune.h")]
@@ -67,6 +90,8 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, debug: bool = Fals
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, out)
+    if not debug:
+        build_binding(verbose)
     return out
 
 

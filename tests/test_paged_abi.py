@@ -1,5 +1,7 @@
 """Refusals of the paged cache's entry points, without a GPU: the C ABI with addresses that are never used, and the
 binding's checks of tensors."""
+import struct
+
 import pytest
 import torch
 
@@ -24,12 +26,17 @@ def cache(**kw):
     return [0 if v is None else v for v in {**CACHE, **kw}.values()]
 
 
-def call(fn, pack, fields, kw, flags):
+# the argument structs of mnb.h as struct formats
+CACHE_FMT = "PPqqqqqqqii"
+FMT = dict(tables="@11P7q", append="@11P" + CACHE_FMT + "12qfi", attention="@7P" + CACHE_FMT + "8qNfi")
+
+
+def call(fn, fmt, fields, kw, flags):
     assert set(kw) <= set(fields)
     vals = []
     for v in {**fields, **kw}.values():
         vals += v if isinstance(v, list) else [0 if v is None else v]
-    return fn(pack(*vals), flags, None)
+    return fn(struct.pack(FMT[fmt], *vals), flags, None)
 
 
 BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(dtype=2), INVALID), (dict(num_pages=0), SHAPE),
@@ -43,7 +50,7 @@ BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(dtype=2), 
 def tables(mnb, flags=0, **kw):
     d = dict(ctx=A, new=A + 64, free=A, start=A, table=A, seq=A + 128, cu=A, slots=A, pos=A, next=A + 4, status=None,
              B=4, T=4, page=16, pages=10, nfree=10, stride=8, blocks=8)
-    return call(mnb._lib.mnb_paged_tables, mnb._pack_tables, d, kw, flags)
+    return call(mnb._lib.mnb_paged_tables, "tables", d, kw, flags)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -63,7 +70,7 @@ def append(mnb, c=None, flags=0, **kw):
     d = dict(q=A, k=A, v=A, o=A + 4096, slots=A, pos=A, cos=A, sin=A, qw=A, kw=A, status=None, cache=c or cache(),
              qt=4096, qh=128, kt=4096, kh=128, vt=4096, vh=128, ot=2048, oh=128, T=4, Hq=16, R=128, num_pos=100,
              eps=1e-6, reserved=0)
-    return call(mnb._lib.mnb_rope_append, mnb._pack_append, d, kw, flags)
+    return call(mnb._lib.mnb_rope_append, "append", d, kw, flags)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -88,7 +95,7 @@ def test_append_refuses_rows_on_one_another(mnb):
 def attention(mnb, c=None, flags=0, **kw):
     d = dict(q=A, out=A, lse=None, table=A, lens=A, ws=A, status=None, cache=c or cache(), qb=2048, qh=128, ob=2048,
              oh=128, stride=8, blocks=8, B=4, Hq=16, nws=1 << 30, scale=0.1, reserved=0)
-    return call(mnb._lib.mnb_paged_attention, mnb._pack_attention, d, kw, flags)
+    return call(mnb._lib.mnb_paged_attention, "attention", d, kw, flags)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -116,13 +123,10 @@ def test_nothing_to_do(mnb):
         assert fn(None, 0, None) == INVALID      # no arguments
 
 
-def test_packed_arguments_have_the_structs_layout(tmp_path):
-    """Sizes and a late offset of the argument structs, as a C compiler lays them out, against the packing."""
+def test_formats_are_the_structs_layout(tmp_path):
+    """Sizes and a late offset of the argument structs, as a C compiler lays them out, against the formats above."""
     import os
-    import struct
     import subprocess
-
-    import int4_block_quantized_matmulnbits_b200 as m
 
     src = tmp_path / "s.c"
     src.write_text('#include <stdio.h>\n#include "mnb.h"\nint main(void) { printf("%zu %zu %zu %zu %zu %zu\\n", '
@@ -132,9 +136,7 @@ def test_packed_arguments_have_the_structs_layout(tmp_path):
     inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
     subprocess.check_call(["gcc", "-I", inc, str(src), "-o", str(tmp_path / "s")])
     got = [int(x) for x in subprocess.check_output([str(tmp_path / "s")]).split()]
-    c = m._CACHE
-    assert got == [struct.calcsize("@" + f) for f in ("11P7q", "11P" + c + "12qfi", "7P" + c + "8qNfi", "11P", "11P" + c,
-                                                      "7P" + c + "8qN")]
+    assert got == [struct.calcsize(f) for f in (*FMT.values(), "@11P", "@11P" + CACHE_FMT, "@7P" + CACHE_FMT + "8qN")]
 
 
 def test_workspace_bytes(mnb):
@@ -182,3 +184,13 @@ def test_tuning_hook_checks_its_argument(mnb):
     for bad in ((-1, 0, 0), (9, 0, 0), (0, -1, 0), (0, 13, 0), (0, 0, -1), (0, 0, 33)):
         assert f(*bad) == INVALID
     assert f(0, 0, 0) == OK
+
+
+def test_binding_takes_other_objects_for_what_they_are(mnb):
+    i, kv = torch.zeros(4, dtype=torch.int32), torch.zeros(3, 16, 2, 64, dtype=torch.float16)
+    for bad in (None, 7, "x", [1, 2]):
+        assert mnb._binding.paged_attention(bad, kv, kv, i, i, 0.1, kv, kv, None, None, 0, None) is None
+        assert mnb._binding.rope_append(bad, kv, kv, bad, kv, i, None, None, None, None, None, None, 0.0, None, 0, None) is None
+        assert mnb._binding.paged_tables(bad, i, i, 1, 1, i, i, i, i, i, i, i, None, 0, None) is None
+    with pytest.raises(TypeError):
+        mnb._binding.paged_attention(1, 2)
