@@ -484,7 +484,7 @@ typedef struct mnb_paged_attention_args {
  * the block table and rows of its last page there may hold anything.
  *   lse fp32 [B][Hq] or NULL.  1 <= Hq <= 4096, Hq % Hkv == 0, 0 <= B <= 4096,
  *   max_blocks * page_size <= 2^31 - 64.
- *   Calls of the same sizes on one GPU model give the same results, bit for bit.
+ *   Calls of the same sizes on one GPU give the same results, bit for bit.
  *   The launch shape follows B, the heads and max_blocks (the lengths are on the
  *   device): a table much wider than the longest request needs costs time; a
  *   view of its first columns serves as well.

@@ -776,13 +776,45 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
     }
 }
 
-constexpr size_t kSmemMax = 227 * 1024 - 256;
-constexpr size_t kSmemSm = 228 * 1024;
+constexpr size_t kSmemMax = 227 * 1024 - 512;   // of a CTA, besides its static shared memory
+constexpr size_t kSmemSm = 228 * 1024;          // of an SM, 1 KB of it for each CTA
 
-// Clusters of `split` CTAs that run at once with `per_sm` CTAs on an SM.  A cluster
-// lives in one of seven parts of the GPU: measured, 14 clusters of 8 CTAs that
-// fill their SMs run at once and a 16th waits for them (11.9 against 20.5 us).
-int64_t clusters_at_once(int sms, int per_sm, int split) { return sms / 7 * per_sm / split * 7; }
+__global__ void occupancy_kernel() {}
+
+// Clusters of `split` CTAs that run at once on the current device with `per_sm`
+// CTAs on an SM, as the driver counts them: a cluster's CTAs share one of the
+// GPU's parts, whose SMs differ in number from GPU to GPU (15 clusters of 8 CTAs
+// with an SM each on one, 14 on another; one more waits for a whole round: 7
+// against 8 requests of 4096 tokens in two heads took 11.9 and 20.5 us).
+int64_t clusters_at_once(int per_sm, int split) {
+    static int known[kMaxDevices][kMaxWarps + 1][kMaxSplit + 1] = {};   // threads that race here write the same
+    static int smem_cache[kMaxDevices] = {};
+    const int guess = device_sm_count() * per_sm / split;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+        return guess;
+    int &n = known[dev][per_sm][split];
+    if (n == 0) {
+        const size_t share = kSmemSm / per_sm - 1024 - 512, smem = share < kSmemMax ? share : kSmemMax;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3((unsigned)split);
+        cfg.blockDim = dim3(32);
+        cfg.dynamicSmemBytes = smem;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)split;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int got = 0;
+        const void *kernel = reinterpret_cast<const void *>(occupancy_kernel);
+        if (ensure_dynamic_smem(kernel, (int)kSmemMax, smem_cache) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess || got < 1)
+            got = guess;
+        n = got;
+    }
+    return n;
+}
 
 // Tuning hook: what is not 0 replaces the rule's choice.
 int g_split = 0, g_warps = 0, g_groups = 0;
@@ -797,17 +829,18 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
     // The shape: an SM has room for kWarpsMost warps' rings.  Of the shapes whose CTAs
     // all run at once, the one with the most warps; of those, where a warp's ring is
     // 16 KB, the one with the most CTAs, as shorter CTAs even out ragged lengths (16
-    // requests of up to 16384: 97 us as 4 x 3 against 101 us as 1 x 12).  More CTAs
+    // requests of up to 16384: 97 us as 4 x 3 against 101 us as 1 x 12; heads of 256
+    // keep three warps or more for the joins of their longer rows).  More CTAs
     // than 1.5 per SM only for work: 4 tiles a warp (16 requests of 128 tokens in 8
     // heads: 5.4 us as 1 x 4, 9.8 as 4 x 4).
     const int most = C::kWarpsMost;
     int split = 1, warps = 0;
     for (int S = 1; S <= kMaxSplit && S <= tiles; S++) {
         int k = 1;
-        while (k <= 6 && all > clusters_at_once(sms, k, S))
+        while (k <= 6 && all > clusters_at_once(k, S))
             k++;
         const int W = most / k;
-        if (k > 6 || W < 1 || (S > 1 && 2 * all * S > 3 * sms && (int64_t)4 * S * W > tiles))
+        if (k > 6 || W < most / 6 || (most < kMaxWarps && W < 3) || (S > 1 && 2 * all * S > 3 * sms && (int64_t)4 * S * W > tiles))
             continue;
         if (S * W > split * warps || (S * W == split * warps && most == kMaxWarps && W >= 3))
             split = S, warps = W;
@@ -827,8 +860,8 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
     warps = g_warps ? g_warps < C::kWarpsMost ? g_warps : C::kWarpsMost : warps;
     // Groups: where the clusters of a few long segments would leave SMs idle, until a warp has 4 tiles.
     int64_t groups = 1;
-    if (all <= clusters_at_once(sms, 1, kMaxSplit) && tiles > 6 * split * warps) {
-        const int64_t want = (tiles - 1) / (4 * split * warps) + 1, room = clusters_at_once(sms, 1, split) / all;
+    if (all <= clusters_at_once(1, kMaxSplit) && tiles > 6 * split * warps) {
+        const int64_t want = (tiles - 1) / (4 * split * warps) + 1, room = clusters_at_once(1, split) / all;
         groups = want < room ? want : room;
     }
     groups = g_groups ? g_groups : groups;
@@ -837,7 +870,7 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
     // A deeper ring where the CTAs leave room for one.
     const size_t stage = (size_t)warps * 2 * C::TILE_BYTES, q_bytes = (size_t)p.rows * C::ROW_BYTES;
     int per_sm = 1;
-    while (per_sm < C::kWarpsMost / warps && all * groups > clusters_at_once(sms, per_sm, split))
+    while (per_sm < C::kWarpsMost / warps && all * groups > clusters_at_once(per_sm, split))
         per_sm++;
     size_t room = kSmemSm / per_sm - 1024 - 512;
     room = room < kSmemMax ? room : kSmemMax;
