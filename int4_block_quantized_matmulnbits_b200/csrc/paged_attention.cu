@@ -56,10 +56,10 @@ struct AttnParams {
     float scale;
 };
 
-// Element type, padded head size and whether D fills it, rows of query heads per segment.  A tile is
-// 8 KB of K and V (16 KB for heads of 256): 16 keys of 128 fp16 entries.
-// Rows are swizzled in shared memory (chunk ^ row % 8), so that reads of eight
-// rows' same chunk meet no bank twice.
+// Element type, padded head size and whether D fills it, rows of query heads per
+// segment.  A tile is 8 KB of K and V (16 KB for heads of 256): 16 keys of 128
+// fp16 entries.  Rows are swizzled in shared memory (chunk ^ row % 8), so that
+// reads of eight rows' same chunk meet no bank twice.
 template <typename T_, int DP_, int ROWS_, bool WHOLE_>
 struct Cfg {
     using T = T_;
@@ -537,7 +537,10 @@ __device__ __forceinline__ float ld_cluster(uint32_t a) {
 }
 __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
@@ -601,7 +604,7 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
     const int kRing = p.stages * 2 * C::TILE_BYTES;   // bytes a warp
     uint8_t *my_ring = smem + (size_t)warp * kRing;
     const uint32_t ring = smem_u32(my_ring);
-    uint8_t *q_rows = smem + (size_t)W * kRing;
+    uint8_t *q_rows = smem + (size_t)W * kRing;   // then the CTA's partial result
     const int S = p.split, P = p.groups, seg = blockIdx.y, b = blockIdx.z;
     const int group = P == 1 ? 0 : quotient(blockIdx.x, p.by_split), rank = blockIdx.x - group * S;
     const int h = p.row_tiles == 1 ? seg : seg / p.row_tiles, r0 = (seg - h * p.row_tiles) * C::ROWS;
@@ -709,14 +712,15 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
     float *group_part = p.partials + ((int64_t)id * P + group) * pf;
 
     // of the CTA's warps
-    float *cta_part = reinterpret_cast<float *>(smem) + pf;   // in warp 0's ring, behind its part
+    float *cta_part = reinterpret_cast<float *>(q_rows);   // every warp is done with the query rows
     {
         const int parts = min(max(t1 - t0, 0), W);
         for (int task = warp; task < tasks; task += W) {
             const int r = row_of(task), c = col_of(task);
             const float *ml = reinterpret_cast<const float *>(smem + (size_t)lane * kRing) + part_at + r;
             float M, L;
-            const float4 o = merge(parts, lane < parts ? ml[0] : -INFINITY, lane < parts ? ml[p.rows] : 0.0f, M, L, [&](int i) {
+            const float m = lane < parts ? ml[0] : -INFINITY, l = lane < parts ? ml[p.rows] : 0.0f;
+            const float4 o = merge(parts, m, l, M, L, [&](int i) {
                 return *reinterpret_cast<const float4 *>(smem + (size_t)i * kRing + (r * p.D + (c < p.D ? c : 0)) * 4);
             });
             if (joined)
@@ -826,13 +830,13 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
     const int64_t all = (int64_t)B * segs;
     const int tiles = (p.cap - 1) / C::TK + 1;   // of the longest request that the table has room for
     p.one_page = p.page % C::TK == 0;
-    // The shape: an SM has room for kWarpsMost warps' rings.  Of the shapes whose CTAs
-    // all run at once, the one with the most warps; of those, where a warp's ring is
-    // 16 KB, the one with the most CTAs, as shorter CTAs even out ragged lengths (16
-    // requests of up to 16384: 97 us as 4 x 3 against 101 us as 1 x 12; heads of 256
-    // keep three warps or more for the joins of their longer rows).  More CTAs
-    // than 1.5 per SM only for work: 4 tiles a warp (16 requests of 128 tokens in 8
-    // heads: 5.4 us as 1 x 4, 9.8 as 4 x 4).
+    // The shape, CTAs of a cluster x warps of a CTA: an SM has room for kWarpsMost
+    // warps' rings.  Of the shapes whose CTAs all run at once, the one with the most
+    // warps; of those, where a warp's ring is 16 KB, the one with the most CTAs, as
+    // shorter CTAs even out ragged lengths (16 requests of up to 16384: 97 us as 4 x 3
+    // against 101 us as 1 x 12; heads of 256 keep three warps or more for the joins of
+    // their longer rows).  More CTAs than 1.5 per SM only for work: 4 tiles a warp (16
+    // requests of 128 tokens in 8 heads: 5.4 us as 1 x 4, 9.8 as 4 x 4).
     const int most = C::kWarpsMost;
     int split = 1, warps = 0;
     for (int S = 1; S <= kMaxSplit && S <= tiles; S++) {
@@ -840,7 +844,8 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
         while (k <= 6 && all > clusters_at_once(k, S))
             k++;
         const int W = most / k;
-        if (k > 6 || W < most / 6 || (most < kMaxWarps && W < 3) || (S > 1 && 2 * all * S > 3 * sms && (int64_t)4 * S * W > tiles))
+        if (k > 6 || W < most / 6 || (most < kMaxWarps && W < 3) ||
+            (S > 1 && 2 * all * S > 3 * sms && (int64_t)4 * S * W > tiles))
             continue;
         if (S * W > split * warps || (S * W == split * warps && most == kMaxWarps && W >= 3))
             split = S, warps = W;
@@ -869,12 +874,14 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
     groups = all * groups > kMaxGroups || groups < 1 ? 1 : groups;
     // A deeper ring where the CTAs leave room for one.
     const size_t stage = (size_t)warps * 2 * C::TILE_BYTES, q_bytes = (size_t)p.rows * C::ROW_BYTES;
+    const size_t part_bytes = (size_t)partial_floats(p.rows, p.D) * 4, tail = q_bytes > part_bytes ? q_bytes : part_bytes;
+    static_assert(2 * 2 * C::TILE_BYTES >= (C::ROWS * (C::DP + 2) + 3) / 4 * 16, "a ring holds its warp's partial result");
     int per_sm = 1;
     while (per_sm < C::kWarpsMost / warps && all * groups > clusters_at_once(per_sm, split))
         per_sm++;
     size_t room = kSmemSm / per_sm - 1024 - 512;
     room = room < kSmemMax ? room : kSmemMax;
-    const size_t fit = (room - q_bytes) / stage;
+    const size_t fit = (room - tail) / stage;
     p.stages = fit < 2 ? 2 : fit > kMaxStages ? kMaxStages : (int)fit;
     // few CTAs: every one for the shortest way; many: none for less than two tiles a warp
     p.least = all * split <= 2 * sms ? 1 : 2 * warps;
@@ -885,7 +892,7 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)(split * groups), (unsigned)segs, (unsigned)B);
     cfg.blockDim = dim3((unsigned)warps * 32);
-    cfg.dynamicSmemBytes = p.stages * stage + q_bytes;
+    cfg.dynamicSmemBytes = p.stages * stage + tail;
     cfg.stream = s;
     cfg.attrs = attr;
     if (split > 1) {
@@ -909,7 +916,8 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
 
 template <typename T, int DP, int ROWS>
 int launch_rows(const AttnParams &p, int B, unsigned flags, cudaStream_t s) {
-    return p.D == DP ? launch_cfg<Cfg<T, DP, ROWS, true>>(p, B, flags, s) : launch_cfg<Cfg<T, DP, ROWS, false>>(p, B, flags, s);
+    return p.D == DP ? launch_cfg<Cfg<T, DP, ROWS, true>>(p, B, flags, s)
+                     : launch_cfg<Cfg<T, DP, ROWS, false>>(p, B, flags, s);
 }
 
 template <typename T, int DP>

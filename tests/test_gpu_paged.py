@@ -254,6 +254,7 @@ CASES = [
     ([333, 17, 250], 6, 2, 200, 16, True),
     ([333, 17, 250], 3, 1, 72, 48, False),
     ([100, 9], 10, 1, 24, 5, False),
+    ([257, 300, 128] * 8, 32, 2, 256, 16, False),   # the largest partial results, in clusters
     ([64] * 97, 4, 2, 128, 16, False),
 ]
 
