@@ -181,8 +181,8 @@ struct AppendParams {
     const int32_t *slots, *pos;
     const float *cos, *sin, *qw, *kw;
     int *status;
-    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;   // token and head strides, elements
-    int64_t page_stride, slot_stride, head_stride;
+    uint32_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;   // token and head strides, elements (at most 2^31)
+    uint32_t page_stride, slot_stride, head_stride;
     int64_t T;
     int Hq, Hkv, D, R, page, num_pos, num_slots;
     int lph, gpt, tpc;   // lanes a head, groups a token, tokens a CTA
@@ -199,22 +199,41 @@ __device__ __forceinline__ void load_v(const float *p, float (&x)[V]) {
         x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
     }
 }
-template <int V>
-__device__ __forceinline__ void load_v(const half *p, float (&x)[V]) {
-    uint32_t u[V / 2];
-    if constexpr (V == 8) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
-    } else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        u[0] = v.x, u[1] = v.y;
+// The same as they lie in memory (16 bytes, or 8 for four of fp16), and their fp32 values.
+template <typename T, int V>
+struct Raw {
+    uint32_t u[V * (int)sizeof(T) / 4];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (sizeof(u) == 16) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            u[0] = v.x, u[1] = v.y;
+        }
     }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (sizeof(u) == 16)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        else
+            *reinterpret_cast<uint2 *>(p) = make_uint2(u[0], u[1]);
+    }
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < V / 2; i++) {
-        const float2 f = __half22float2(u32_as_h2(u[i]));
-        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        for (int i = 0; i < (int)(sizeof(u) / 4); i++)
+            u[i] = 0;
     }
-}
+    __device__ __forceinline__ void get(float (&x)[V]) const {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(u) / 4); i++)
+            if constexpr (sizeof(T) == 4) {
+                x[i] = __uint_as_float(u[i]);
+            } else {
+                const float2 f = __half22float2(u32_as_h2(u[i]));
+                x[2 * i] = f.x, x[2 * i + 1] = f.y;
+            }
+    }
+};
 template <int V>
 __device__ __forceinline__ void store_v(float *p, const float (&x)[V]) {
 #pragma unroll
@@ -233,6 +252,11 @@ __device__ __forceinline__ void store_v(half *p, const float (&x)[V]) {
         *reinterpret_cast<uint2 *>(p) = make_uint2(u[0], u[1]);
 }
 
+// n x stride in 64 bits, one instruction.
+__device__ __forceinline__ int64_t wide(int n, uint32_t stride) { return (int64_t)((uint64_t)(uint32_t)n * stride); }
+
+constexpr int kAppendThreads = 256;
+
 // A group of `lph` lanes (a power of two, up to a warp) per head, 2 V entries a
 // lane: a rotary lane holds V entries of the first half and their V partners of
 // the second, so norm, rotation and store stay in registers; one rounding, at the
@@ -240,8 +264,6 @@ __device__ __forceinline__ void store_v(half *p, const float (&x)[V]) {
 // position, cosines and sines are loaded once for the heads that a group takes.
 // Bound by bandwidth for many tokens, by the chain slot / position -> cosines ->
 // store for few.
-constexpr int kAppendThreads = 256;
-
 template <typename T, int V>
 __global__ void __launch_bounds__(kAppendThreads, V == 8 ? 4 : 6) rope_append_kernel(const __grid_constant__ AppendParams p) {
     pdl_wait();
@@ -249,7 +271,7 @@ __global__ void __launch_bounds__(kAppendThreads, V == 8 ? 4 : 6) rope_append_ke
     const int l = threadIdx.x & (p.lph - 1), group = threadIdx.x / p.lph;
     const unsigned mask = (p.lph == 32 ? 0xffffffffu : (1u << p.lph) - 1) << (threadIdx.x & 31 & ~(p.lph - 1));
     const int tok = quotient(group, p.by_gpt), h0 = group - tok * p.gpt;
-    const int64_t t = (int64_t)blockIdx.x * p.tpc + tok;
+    const int t = blockIdx.x * p.tpc + tok;   // below 2^30 + 256
     if (tok >= p.tpc || t >= p.T)
         return;
     const int heads = p.Hq + 2 * p.Hkv;
@@ -258,19 +280,15 @@ __global__ void __launch_bounds__(kAppendThreads, V == 8 ? 4 : 6) rope_append_ke
     // What no other load decides on is requested first: slot, position and the first head.
     const int slot = p.slots[t];
     const int pos = p.R > 0 ? p.pos[t] : 0;
-    float a[V], b[V];
+    Raw<T, V> ra, rb;   // of the next head to work on
     auto load = [&](int i) {
         const bool q = i < p.Hq, k = i < p.Hq + p.Hkv;
-        const int64_t ts = q ? p.q_ts : k ? p.k_ts : p.v_ts, hs = q ? p.q_hs : k ? p.k_hs : p.v_hs;
-        const T *src = (const T *)(q ? p.q : k ? p.k : p.v) + t * ts + (q ? i : k ? i - p.Hq : i - p.Hq - p.Hkv) * hs;
-        if (live) {
-            load_v<V>(src + e0, a);
-            load_v<V>(src + e1, b);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; j++)
-                a[j] = b[j] = 0.0f;
-        }
+        const uint32_t ts = q ? p.q_ts : k ? p.k_ts : p.v_ts, hs = q ? p.q_hs : k ? p.k_hs : p.v_hs;
+        const T *src = (const T *)(q ? p.q : k ? p.k : p.v) + wide(t, ts) + wide(q ? i : k ? i - p.Hq : i - p.Hq - p.Hkv, hs);
+        if (live)
+            ra.load(src + e0), rb.load(src + e1);
+        else
+            ra.zero(), rb.zero();
     };
     load(h0);
     const bool pos_ok = p.R == 0 || (pos >= 0 && pos < p.num_pos);
@@ -285,11 +303,24 @@ __global__ void __launch_bounds__(kAppendThreads, V == 8 ? 4 : 6) rope_append_ke
     int64_t cache_at = 0;
     if (slot_ok) {
         const int page = quotient(slot, p.by_page);
-        cache_at = page * p.page_stride + (int64_t)(slot - page * p.page) * p.slot_stride;
+        cache_at = wide(page, p.page_stride) + wide(slot - page * p.page, p.slot_stride);
     }
     for (int i = h0;;) {
         const int kind = i < p.Hq ? 0 : i < p.Hq + p.Hkv ? 1 : 2;   // q, k, v
+        const int h = kind == 0 ? i : kind == 1 ? i - p.Hq : i - p.Hq - p.Hkv;
+        T *dst = kind == 0 ? (T *)p.q_out + wide(t, p.o_ts) + wide(h, p.o_hs)
+                           : (T *)(kind == 1 ? p.k_cache : p.v_cache) + cache_at + wide(h, p.head_stride);
+        if (kind == 2) {   // as it is
+            if (live && slot_ok)
+                ra.store(dst + e0), rb.store(dst + e1);
+            if ((i += p.gpt) >= heads)
+                return;
+            load(i);
+            continue;
+        }
         const float *w = kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr;
+        float a[V], b[V];
+        ra.get(a), rb.get(b);
         if (w) {
             float ss = 0.0f;
 #pragma unroll
@@ -307,7 +338,7 @@ __global__ void __launch_bounds__(kAppendThreads, V == 8 ? 4 : 6) rope_append_ke
                     a[j] = a[j] * r * x[j], b[j] = b[j] * r * y[j];
             }
         }
-        if (rot && kind < 2 && pos_ok) {
+        if (rot && pos_ok) {
 #pragma unroll
             for (int j = 0; j < V; j++) {
                 const float x = a[j], y = b[j];
@@ -321,9 +352,6 @@ __global__ void __launch_bounds__(kAppendThreads, V == 8 ? 4 : 6) rope_append_ke
                 a[j] = b[j] = 0.0f;
         }
         if (live && (kind == 0 || slot_ok)) {
-            const int64_t hs = kind == 0 ? p.o_hs : p.head_stride;
-            T *dst = (T *)(kind == 0 ? p.q_out : kind == 1 ? p.k_cache : p.v_cache) + (kind == 0 ? t * p.o_ts : cache_at) +
-                     (kind == 0 ? i : kind == 1 ? i - p.Hq : i - p.Hq - p.Hkv) * hs;
             store_v<V>(dst + e0, a);
             store_v<V>(dst + e1, b);
         }
@@ -404,8 +432,10 @@ int launch_rope_append(const void *q, int64_t q_ts, int64_t q_hs, const void *k,
     AppendParams p;
     p.q = q, p.k = k, p.v = v, p.q_out = q_out, p.k_cache = c->k, p.v_cache = c->v;
     p.slots = slots, p.pos = pos, p.cos = cos, p.sin = sin, p.qw = qw, p.kw = kw, p.status = status;
-    p.q_ts = q_ts, p.q_hs = q_hs, p.k_ts = k_ts, p.k_hs = k_hs, p.v_ts = v_ts, p.v_hs = v_hs, p.o_ts = o_ts, p.o_hs = o_hs;
-    p.page_stride = c->page_stride, p.slot_stride = c->slot_stride, p.head_stride = c->head_stride;
+    p.q_ts = (uint32_t)q_ts, p.q_hs = (uint32_t)q_hs, p.k_ts = (uint32_t)k_ts, p.k_hs = (uint32_t)k_hs;
+    p.v_ts = (uint32_t)v_ts, p.v_hs = (uint32_t)v_hs, p.o_ts = (uint32_t)o_ts, p.o_hs = (uint32_t)o_hs;
+    p.page_stride = (uint32_t)c->page_stride, p.slot_stride = (uint32_t)c->slot_stride;
+    p.head_stride = (uint32_t)c->head_stride;
     p.T = T;
     p.Hq = Hq, p.Hkv = (int)c->num_heads, p.D = (int)c->head_dim, p.R = R, p.page = (int)c->page_size;
     p.inv_D = 1.0f / (float)p.D, p.by_page = div_by((uint32_t)c->page_size);
