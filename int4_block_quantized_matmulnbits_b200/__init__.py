@@ -1,7 +1,7 @@
 """MatMulNBits (weight-only int4, block-quantized) for NVIDIA B200 -- Python binding.
 
-A thin layer (ctypes, and ``_binding.so`` for the paged cache's calls) over ``libmnb.so`` (the sm_100a kernels and their C ABI,
-declared in ``include/mnb.h``).  Every function here has the name of the C
+A thin layer over ``libmnb.so`` (the sm_100a kernels and their C ABI, declared in
+``include/mnb.h``): ctypes, and ``_binding.so`` for the paged cache's calls.  Every function here has the name of the C
 entry point it calls and only marshals arguments: torch tensors become device
 pointers, dtypes become ``mnb_dtype`` values, the stream defaults to torch's
 current stream.  All arithmetic runs in the CUDA kernels; there is no CPU path.

@@ -262,8 +262,9 @@ constexpr int kAppendThreads = 256;
 // the second, so norm, rotation and store stay in registers; one rounding, at the
 // store.  A token's heads are spread over `gpt` groups of one CTA, so its slot,
 // position, cosines and sines are loaded once for the heads that a group takes.
-// Bound by bandwidth for many tokens, by the chain slot / position -> cosines ->
-// store for few.
+// Bound by the chain slot / position -> cosines -> store for few tokens (2.5 us for
+// one), by instruction issue and DRAM for many (8191 fp32 tokens: 5200 GB/s, 8000
+// fp16 tokens: 4000 GB/s).
 template <typename T, int V>
 __global__ void __launch_bounds__(kAppendThreads, V == 8 ? 4 : 6) rope_append_kernel(const __grid_constant__ AppendParams p) {
     pdl_wait();
@@ -392,7 +393,7 @@ int launch_append(AppendParams p, unsigned flags, cudaStream_t s) {
     const int groups = kAppendThreads / p.lph;
     // With tokens for every SM a group takes two heads of 16-byte pairs, or three of
     // 8-byte (fp16) or fp32 ones: what the lanes work out per token is then shared
-    // (1024 fp16 tokens: 7.0 us, 7.9 with one head; 8191 fp32 tokens: 27.8 us, 29.9).
+    // (1024 fp16 tokens: 7.0 us, 7.9 with one head; 8191 fp32 tokens: 28 us, 30).
     const int rounds = max((heads + groups - 1) / groups, p.T < 2 * device_sm_count() ? 1 : V == 8 ? 2 : 3);
     p.gpt = (heads + rounds - 1) / rounds;   // as many heads a group for all groups, or one fewer
     p.by_gpt = div_by((uint32_t)p.gpt);

@@ -359,6 +359,28 @@ def test_attention_one_workspace_for_all_and_same_bits(mnb, cuda_dev):
     assert int(ws[:1024].sum()) == 0
 
 
+def test_attention_on_two_streams_at_once(mnb, cuda_dev):
+    """Calls that overlap on two streams, a workspace each: the bits of the same calls one after the other."""
+    mnb._lib.mnb_tune_paged_attention(4, 4, 3)      # groups, so that the workspaces are used
+    try:
+        cases = [paged_case(20 + i, [n, 300], 8, 2, 128, 16, F16) for i, n in enumerate((4000, 2500))]
+        want = [run_attn(mnb, cuda_dev, c, 0.1) for c in cases]
+        dev = [[on_dev(t, cuda_dev) for t in c] for c in cases]
+        ws = [torch.zeros(mnb.mnb_paged_attention_workspace_bytes(2, 8, 2, 128), dtype=torch.uint8, device=cuda_dev)
+              for _ in cases]
+        streams = [torch.cuda.Stream() for _ in cases]
+        outs = [[torch.empty(2, 8, 128, dtype=F16, device=cuda_dev) for _ in range(30)] for _ in cases]
+        torch.cuda.synchronize()
+        for r in range(30):
+            for (q, k, v, table, lens), w, s, o in zip(dev, ws, streams, outs):
+                mnb.mnb_paged_attention(q, k, v, table, lens, 0.1, o[r], w, stream=s)
+        torch.cuda.synchronize()
+        for (ref, _), o in zip(want, outs):
+            assert all(torch.equal(x.cpu(), ref) for x in o)
+    finally:
+        mnb._lib.mnb_tune_paged_attention(0, 0, 0)
+
+
 def test_attention_offsets_beyond_32_bits(mnb, cuda_dev, shape):
     """Pages more than 2^31 elements into the pool."""
     ps, H, D = 16, 8, 128
