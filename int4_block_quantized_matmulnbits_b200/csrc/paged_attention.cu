@@ -566,35 +566,36 @@ __device__ __forceinline__ void cp_wait_rt(int n) {
     }
 }
 
-// Joins up to 32 partial results of a row for four outputs a lane: lane i brings
-// the maximum m and sum l of part i (-inf and 0 behind the last), load(i) the
-// lane's outputs of part i.  Returns the outputs, M and L of the whole.
-template <typename Load>
-__device__ __forceinline__ float4 merge(int parts, float m, float l, float &M, float &L, Load load) {
-    float4 v[4];
-#pragma unroll
-    for (int u = 0; u < 4; u++)
-        if (u < parts)
-            v[u] = load(u);
-    M = m;
-#pragma unroll
-    for (int x = 16; x; x >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    const float w = ex2(m - (M == -INFINITY ? 0.0f : M));
-    L = l * w;
-#pragma unroll
-    for (int x = 16; x; x >>= 1)
-        L += __shfl_xor_sync(0xffffffffu, L, x);
+// Joins partial results of a row for four outputs a lane: ml(i) is the maximum and
+// sum of part i, out(i) the lane's outputs of it.  Four parts are on their way at a
+// time and every lane works out every weight: no lane waits for another (16
+// requests of 128 tokens: 5.15 us, 5.4 with weights by shuffle, 5.5 with eight).
+template <typename MaxSum, typename Out>
+__device__ __forceinline__ float4 merge(int parts, float &M, float &L, MaxSum ml, Out out) {
+    constexpr int N = 4;
     float4 o = make_float4(0, 0, 0, 0);
-    for (int i = 0; i < parts; i += 4) {
+    M = -INFINITY, L = 0.0f;
+    for (int i = 0; i < parts; i += N) {
+        float2 s[N];
+        float4 v[N];
 #pragma unroll
-        for (int u = 0; u < 4; u++)
+        for (int u = 0; u < N; u++)
             if (i + u < parts)
-                fma4(o, __shfl_sync(0xffffffffu, w, i + u), v[u]);
+                s[u] = ml(i + u), v[u] = out(i + u);
+        float mn = M;
 #pragma unroll
-        for (int u = 0; u < 4; u++)
-            if (i + 4 + u < parts)
-                v[u] = load(i + 4 + u);
+        for (int u = 0; u < N; u++)
+            mn = i + u < parts ? fmaxf(mn, s[u].x) : mn;
+        const float base = mn == -INFINITY ? 0.0f : mn, old = ex2(M - base);
+        M = mn, L *= old;
+        o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+#pragma unroll
+        for (int u = 0; u < N; u++)
+            if (i + u < parts) {
+                const float w = ex2(s[u].x - base);
+                L = fmaf(w, s[u].y, L);
+                fma4(o, w, v[u]);
+            }
     }
     return o;
 }
@@ -732,12 +733,12 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
         const int parts = min(max(t1 - t0, 0), W);
         for (int task = warp; task < tasks; task += W) {
             const int r = row_of(task), c = col_of(task);
-            const float *ml = reinterpret_cast<const float *>(smem + (size_t)lane * kRing) + part_at + r;
             float M, L;
-            const float m = lane < parts ? ml[0] : -INFINITY, l = lane < parts ? ml[p.rows] : 0.0f;
-            const float4 o = merge(parts, m, l, M, L, [&](int i) {
-                return *reinterpret_cast<const float4 *>(smem + (size_t)i * kRing + (r * p.D + (c < p.D ? c : 0)) * 4);
-            });
+            const float *at = reinterpret_cast<const float *>(smem) + part_at + r;
+            const float *from = reinterpret_cast<const float *>(smem) + r * p.D + (c < p.D ? c : 0);
+            const float4 o = merge(
+                parts, M, L, [&](int i) { return make_float2(at[i * (kRing / 4)], at[i * (kRing / 4) + p.rows]); },
+                [&](int i) { return *reinterpret_cast<const float4 *>(from + i * (kRing / 4)); });
             if (joined)
                 keep(cta_part, r, c, o, M, L);
             else if (used_groups > 1)
@@ -753,12 +754,15 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
         const uint32_t at = smem_u32(cta_part);
         for (int task = warp * S + rank; task < tasks; task += W * S) {
             const int r = row_of(task), c = col_of(task);
-            const uint32_t ml = cluster_map(at + (part_at + r) * 4, lane < parts ? lane : rank);
-            const float m = lane < parts ? ld_cluster(ml) : -INFINITY, l = lane < parts ? ld_cluster(ml + p.rows * 4) : 0.0f;
+            const uint32_t ml = at + (part_at + r) * 4, from = at + (r * p.D + (c < p.D ? c : 0)) * 4;
             float M, L;
-            const float4 o = merge(parts, m, l, M, L, [&](int i) {
-                return ld_cluster4(cluster_map(at + (r * p.D + (c < p.D ? c : 0)) * 4, i));
-            });
+            const float4 o = merge(
+                parts, M, L,
+                [&](int i) {
+                    const uint32_t m = cluster_map(ml, i);
+                    return make_float2(ld_cluster(m), ld_cluster(m + p.rows * 4));
+                },
+                [&](int i) { return ld_cluster4(cluster_map(from, i)); });
             if (used_groups > 1)
                 keep(group_part, r, c, o, M, L);
             else
@@ -782,14 +786,16 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
         const float *first = p.partials + (int64_t)id * P * pf;
         for (int task = warp; task < tasks; task += W) {
             const int r = row_of(task), c = col_of(task);
-            float m = -INFINITY, l = 0.0f, M, L;
-            if (lane < used_groups) {
-                m = __ldcg(first + (int64_t)lane * pf + part_at + r);
-                l = __ldcg(first + (int64_t)lane * pf + part_at + p.rows + r);
-            }
-            const float4 o = merge(used_groups, m, l, M, L, [&](int i) {
-                return __ldcg(reinterpret_cast<const float4 *>(first + (int64_t)i * pf + r * p.D + (c < p.D ? c : 0)));
-            });
+            float M, L;
+            const float4 o = merge(
+                used_groups, M, L,
+                [&](int i) {
+                    const float *ml = first + (int64_t)i * pf + part_at + r;
+                    return make_float2(__ldcg(ml), __ldcg(ml + p.rows));
+                },
+                [&](int i) {
+                    return __ldcg(reinterpret_cast<const float4 *>(first + (int64_t)i * pf + r * p.D + (c < p.D ? c : 0)));
+                });
             write(r, c, o, M, L);
         }
     }
