@@ -103,18 +103,40 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t &r0, uint32_t &r1, u
                  : "r"(a)
                  : "memory");
 }
-__device__ __forceinline__ float4 lds4(uint32_t a) {
-    float4 r;
-    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(a) : "memory");
+// Four fp32 values as two pairs, for the instructions that take two at a time
+// (each value rounded as by the scalar instruction).
+struct Quad {
+    unsigned long long lo, hi;
+};
+__device__ __forceinline__ Quad lds_quad(uint32_t a) {
+    Quad r;
+    asm volatile("ld.shared.v2.u64 {%0,%1}, [%2];" : "=l"(r.lo), "=l"(r.hi) : "r"(a) : "memory");
     return r;
+}
+__device__ __forceinline__ unsigned long long pair(float x, float y) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1,%2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(unsigned long long p) {
+    float2 r;
+    asm("mov.b64 {%0,%1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
-}
-__device__ __forceinline__ float dot(float4 a, float4 b, float c) {
-    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
 }
 __device__ __forceinline__ void fma4(float4 &c, float s, float4 v) {
     c.x = fmaf(s, v.x, c.x), c.y = fmaf(s, v.y, c.y), c.z = fmaf(s, v.z, c.z), c.w = fmaf(s, v.w, c.w);
@@ -307,7 +329,8 @@ struct Acc<C, true> {
     }
 };
 
-// fp32: every product and sum in fp32 on the CUDA cores, eight keys at a time.
+// fp32: every product and sum in fp32 on the CUDA cores, two at a time, eight keys
+// at a time.
 // Scores: a lane holds key lane % 8 and a quarter of the chunks, two shuffles
 // add the quarters.  Output: a lane holds whole columns; a row's probabilities
 // come by shuffle.
@@ -319,8 +342,8 @@ struct Acc<C, false> {
     static constexpr float kSumScale = 1.0f;
     static constexpr int QC = C::NCH / 4;                   // chunks of a query row that a lane needs
     static constexpr bool QREG = C::ROWS * QC <= 16;        // they stay in registers
-    float4 o[C::ROWS][PER];
-    float4 q[QREG ? C::ROWS : 1][QREG ? QC : 1];
+    Quad o[C::ROWS][PER];
+    Quad q[QREG ? C::ROWS : 1][QREG ? QC : 1];
     float m[C::ROWS], l[C::ROWS];
 
     __device__ __forceinline__ void open(uint32_t qs, int rows) {
@@ -330,12 +353,12 @@ struct Acc<C, false> {
             for (int r = 0; r < C::ROWS; r++)
 #pragma unroll
                 for (int c = 0; c < QC; c++)
-                    q[r][c] = lds4(qs + C::at(min(r, rows - 1), c * 4 + quarter));
+                    q[r][c] = lds_quad(qs + C::at(min(r, rows - 1), c * 4 + quarter));
 #pragma unroll
         for (int r = 0; r < C::ROWS; r++) {
 #pragma unroll
             for (int c = 0; c < PER; c++)
-                o[r][c] = make_float4(0, 0, 0, 0);
+                o[r][c] = {0, 0};
             m[r] = -INFINITY;
             l[r] = 0.0f;
         }
@@ -349,23 +372,28 @@ struct Acc<C, false> {
 
     __device__ __forceinline__ void eight(uint32_t ks, uint32_t vs, uint32_t qs, int rows, int D, uint32_t valid, float scale2) {
         const int lane = threadIdx.x & 31, key = lane & 7, quarter = lane >> 3;
-        float s[C::ROWS] = {};
+        float s[C::ROWS];
+        unsigned long long s2[C::ROWS] = {};   // even and odd entries
 #pragma unroll(QREG ? QC : 4)
         for (int c = 0; c < QC; c++) {
             if (!C::WHOLE && c * 16 >= D)
                 break;
             const int ch = c * 4 + quarter;
-            float4 k = lds4(ks + C::at(key, ch));
+            Quad k = lds_quad(ks + C::at(key, ch));
             if (!C::WHOLE && ch * 4 >= D)   // columns that nothing has written
-                k = make_float4(0, 0, 0, 0);
+                k = {0, 0};
 #pragma unroll
-            for (int r = 0; r < C::ROWS; r++)
-                s[r] = dot(k, QREG ? q[QREG ? r : 0][QREG ? c : 0] : lds4(qs + C::at(min(r, rows - 1), ch)), s[r]);
+            for (int r = 0; r < C::ROWS; r++) {
+                const Quad qr = QREG ? q[QREG ? r : 0][QREG ? c : 0] : lds_quad(qs + C::at(min(r, rows - 1), ch));
+                s2[r] = fma2(k.hi, qr.hi, fma2(k.lo, qr.lo, s2[r]));
+            }
         }
         const bool ok = (valid >> key) & 1;
         bool over = false;
 #pragma unroll
         for (int r = 0; r < C::ROWS; r++) {
+            const float2 both = unpair(s2[r]);
+            s[r] = both.x + both.y;
             s[r] += __shfl_xor_sync(0xffffffffu, s[r], 8);
             s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
             s[r] = ok ? s[r] * scale2 : -INFINITY;
@@ -383,7 +411,7 @@ struct Acc<C, false> {
                 l[r] *= alpha;
 #pragma unroll
                 for (int c = 0; c < PER; c++)
-                    o[r][c].x *= alpha, o[r][c].y *= alpha, o[r][c].z *= alpha, o[r][c].w *= alpha;
+                    o[r][c] = {mul2(o[r][c].lo, pair(alpha, alpha)), mul2(o[r][c].hi, pair(alpha, alpha))};
             }
         }
 #pragma unroll
@@ -395,16 +423,17 @@ struct Acc<C, false> {
 #pragma unroll
         for (int j = 0; j < 8; j += KSPLIT) {
             const int kj = j + sub;
-            float4 v[PER];
+            Quad v[PER];
 #pragma unroll
             for (int c = 0; c < PER; c++)
-                v[c] = lds4(vs + C::at(kj, col + c * 32));
+                v[c] = lds_quad(vs + C::at(kj, col + c * 32));
 #pragma unroll
             for (int r = 0; r < C::ROWS; r++) {
                 const float pr = __shfl_sync(0xffffffffu, s[r], kj);
+                const unsigned long long p2 = pair(pr, pr);
 #pragma unroll
                 for (int c = 0; c < PER; c++)
-                    fma4(o[r][c], pr, v[c]);
+                    o[r][c] = {fma2(p2, v[c].lo, o[r][c].lo), fma2(p2, v[c].hi, o[r][c].hi)};
             }
         }
     }
@@ -419,10 +448,10 @@ struct Acc<C, false> {
             for (int c = 0; c < PER; c++)
 #pragma unroll
                 for (int x = LPR; x < 32; x <<= 1) {
-                    o[r][c].x += __shfl_xor_sync(0xffffffffu, o[r][c].x, x);
-                    o[r][c].y += __shfl_xor_sync(0xffffffffu, o[r][c].y, x);
-                    o[r][c].z += __shfl_xor_sync(0xffffffffu, o[r][c].z, x);
-                    o[r][c].w += __shfl_xor_sync(0xffffffffu, o[r][c].w, x);
+                    float2 a = unpair(o[r][c].lo), b = unpair(o[r][c].hi);
+                    a.x += __shfl_xor_sync(0xffffffffu, a.x, x), a.y += __shfl_xor_sync(0xffffffffu, a.y, x);
+                    b.x += __shfl_xor_sync(0xffffffffu, b.x, x), b.y += __shfl_xor_sync(0xffffffffu, b.y, x);
+                    o[r][c] = {pair(a.x, a.y), pair(b.x, b.y)};
                 }
         }
     }
@@ -435,8 +464,10 @@ struct Acc<C, false> {
                 break;
 #pragma unroll
             for (int c = 0; c < PER; c++)
-                if (lane < LPR && (col + c * 32) * 4 < D)
-                    *reinterpret_cast<float4 *>(sl + r * D + (col + c * 32) * 4) = o[r][c];
+                if (lane < LPR && (col + c * 32) * 4 < D) {
+                    const float2 a = unpair(o[r][c].lo), b = unpair(o[r][c].hi);
+                    *reinterpret_cast<float4 *>(sl + r * D + (col + c * 32) * 4) = make_float4(a.x, a.y, b.x, b.y);
+                }
             if (lane == 0) {
                 sl[rows * D + r] = m[r];
                 sl[rows * D + rows + r] = l[r];
@@ -834,8 +865,10 @@ int64_t clusters_at_once(int per_sm, int split) {
         int got = 0;
         const void *kernel = reinterpret_cast<const void *>(occupancy_kernel);
         if (ensure_dynamic_smem(kernel, (int)kSmemMax, smem_cache) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess || got < 1)
+            cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) != cudaSuccess || got < 1) {
+            (void)cudaGetLastError();   // a failed query is no error of the call's
             got = guess;
+        }
         n = got;
     }
     return n;
