@@ -8,6 +8,9 @@ index checks in the kernels listed in DEBUG_SOURCES.
 Each .cu file compiles to an object under _build/, then one shared library is
 linked next to this file.  CUDA runtime is linked statically, so the library
 only needs the NVIDIA driver at run time.
+
+_binding.so, linked next to it with g++, is the Python module that makes the
+paged cache's calls (csrc/binding.cpp); it needs the torch it was built with.
 """
 from __future__ import annotations
 
