@@ -185,7 +185,9 @@ class PagedCache:
 
     def end(self, stream=None):
         """The step's lengths and free-list position become current."""
-        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext():
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))   # a handle, as the library's calls take it
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             self.lens.copy_(self.new_lens)
             self.start.copy_(self.next)
 

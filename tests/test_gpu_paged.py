@@ -594,3 +594,42 @@ def test_pass_with_attention(mnb, cuda_dev, fused, kind, dtype):
             u = 2.0 ** -11 if dtype == F16 else 2.0 ** -24
             more = 4 * u * reach + 2 * (D / 2 + 8) * 2.0 ** -22 * reach
             assert bool(((out.cpu().double() - ref).abs() <= t_out + 2 * more[..., None] * spread).all())
+
+
+def test_cache_steps_on_a_stream_by_its_handle(mnb, cuda_dev):
+    """begin, layer and end on a side stream given as a Stream and as its handle: the lengths advance there."""
+    from int4_block_quantized_matmulnbits_b200 import step
+
+    cache = step.PagedCache(1, 2, 2, 1, 64, 64)
+    gen = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(2, h, 64, generator=gen).to(F16).to(cuda_dev) for h in (2, 1, 1))
+    out = torch.empty(2, 2, 64, dtype=F16, device=cuda_dev)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(20):
+        st = s if i % 2 else s.cuda_stream
+        cache.begin(stream=st)
+        cache.layer(0, q, k, v, out, stream=st)
+        cache.end(st)
+    torch.cuda.synchronize()
+    cache.check()
+    assert cache.lens.cpu().tolist() == [20, 20]
+    # equal keys: every probability 1/20, the output is v
+    assert float((out.float() - v.float()).abs().max()) <= 2.0 ** -10 * float(v.abs().max())
+
+
+def test_cache_that_is_full_says_so(mnb, cuda_dev):
+    from int4_block_quantized_matmulnbits_b200 import step
+
+    cache = step.PagedCache(1, 2, 2, 1, 64, max_len=32, page_size=16, pages=3)
+    x = torch.zeros(2, 2, 64, dtype=F16, device=cuda_dev)
+    out = torch.empty_like(x)
+    for i in range(18):
+        cache.begin()
+        cache.layer(0, x, x[:, :1], x[:, :1], out)
+        cache.end()
+    # the fourth page is missing: the second request stands still at 16 tokens, the first goes on
+    assert cache.lens.cpu().tolist() == [18, 16]
+    with pytest.raises(RuntimeError, match="status 4"):
+        cache.check()
+    cache.check()
