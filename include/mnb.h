@@ -476,8 +476,9 @@ typedef struct mnb_paged_attention_args {
  * query head i reads KV head i / (Hq / Hkv)).  With n = seq_lens[b] and j < n,
  *   s_j = scale * q[b][i] . k_j,  lse[b][i] = log sum_j exp(s_j) (natural log),
  *   out[b][i] = sum_j exp(s_j - lse) v_j.
- * Scores, softmax statistics and sums are fp32; with fp16, the probabilities
- * are rounded to fp16 for their product with V.  n = 0: out = 0, lse = -inf
+ * Scores, softmax statistics and sums are fp32; with fp16, a probability enters
+ * its product with V as two fp16 numbers, which keep 21 bits of it and all that
+ * is above 2^-34 of the largest.  n = 0: out = 0, lse = -inf
  * (a batch padded to B requests).  n above max_blocks * page_size counts as
  * that, n below 0 as 0 (status bit 1); keys of a page id outside the pool are
  * left out (bit 0).  Nothing behind a request's n tokens is read: entries of

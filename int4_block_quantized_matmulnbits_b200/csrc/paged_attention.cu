@@ -138,6 +138,19 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Two numbers of 0 or above (or NaN) as sums of two fp16 numbers each, within 2^-21
+// of them and 2^-25: the first rounded towards zero, `lo` the rest.  Where the first
+// is above 0 so is the rest (at least 2^-24), so that products of both with an
+// infinity are that infinity and not 0 times it.
+__device__ __forceinline__ uint32_t split2(float x, float y, uint32_t &lo) {
+    uint32_t hi;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
+    const half2 h = u32_as_h2(hi);
+    const float2 f = __half22float2(h);
+    const half2 least = __hmin2(h, u32_as_h2(0x00010001u));
+    lo = h2_as_u32(__hmax2(__floats2half2_rn(x - f.x, y - f.y), least));
+    return hi;
+}
 __device__ __forceinline__ void fma4(float4 &c, float s, float4 v) {
     c.x = fmaf(s, v.x, c.x), c.y = fmaf(s, v.y, c.y), c.z = fmaf(s, v.z, c.z), c.w = fmaf(s, v.w, c.w);
 }
@@ -167,13 +180,18 @@ struct Acc;
 
 // fp16: S^T = K Q^T and O^T += V^T P^T as m16n8k16 products: keys, then head
 // entries are the 16 rows, up to 8 query heads the 8 columns (the grouped heads
-// of one KV head seldom fill more).  P is rounded to fp16 for the second
-// product, scaled so that the reference maximum is at 2^SHIFT: its largest
-// values stay below 2^15, and terms down to 2^-24 of the largest keep their 11
-// bits.  l is summed from the unrounded fp32 values.
+// of one KV head seldom fill more).  P enters the second product as two fp16
+// numbers, which keep 21 of fp32's bits, scaled so that the reference maximum is
+// at 2^SHIFT: its largest values stay below 2^15, and what is lost of any term is
+// below 2^-34 of the largest.  l is summed from the unrounded fp32 values.  Up to
+// four query heads stand in the columns twice, and the second four take the rest
+// of P: then both parts are one product (32 requests of up to 4096 in 8 heads of
+// 80: 42.5 us, 44.0 with two products, 42.0 with P rounded to fp16; 16 heads on a
+// KV head of 256, 24 requests of up to 4001, two products: 40.8 us, 37.3 rounded).
 template <typename C>
 struct Acc<C, true> {
-    static constexpr int NT = C::ROWS / 8, KB = C::TK / 16, KS = C::DP / 16;
+    static constexpr bool TWICE = C::ROWS == 4;
+    static constexpr int NT = TWICE ? 1 : C::ROWS / 8, KB = C::TK / 16, KS = C::DP / 16;
     static constexpr float SHIFT = 10.0f;
     static constexpr float kSumScale = 1.0f / 1024.0f;   // 2^-SHIFT
     float o[KS][NT][4];        // entry 16 i + lane / 4 (+ 8), heads 2 (lane % 4) and the next
@@ -184,7 +202,7 @@ struct Acc<C, true> {
     __device__ __forceinline__ void open(uint32_t qs, int rows) {
         const int lane = threadIdx.x & 31, i = lane >> 3;
         if constexpr (NT == 1) {
-            const int r = min(lane & 7, rows - 1);
+            const int r = min(lane & (TWICE ? 3 : 7), rows - 1);
 #pragma unroll
             for (int kk = 0; kk < KS; kk += 2)
                 ldsm4(qs + C::at(r, kk * 2 + i), q[kk][0][0], q[kk][0][1], q[kk + 1][0][0],
@@ -266,7 +284,7 @@ struct Acc<C, true> {
                         o[k][t][c] *= alpha, o[k][t][c + 2] *= alpha;
                 }
         }
-        uint32_t p[KB][NT][2];
+        uint32_t p[KB][NT][2], p_lo[KB][NT][2];
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             const float b0 = m[t][0] == -INFINITY ? 0.0f : m[t][0] - SHIFT;
@@ -277,7 +295,11 @@ struct Acc<C, true> {
                 for (int h = 0; h < 2; h++) {
                     const float x = ex2(s[b][t][2 * h] - b0), y = ex2(s[b][t][2 * h + 1] - b1);
                     l[t][0] += x, l[t][1] += y;
-                    p[b][t][h] = transpose8(h2_as_u32(__floats2half2_rn(x, y)));
+                    uint32_t lo;
+                    const uint32_t hi = split2(x, y, lo);
+                    p[b][t][h] = transpose8(TWICE && (lane & 2) ? lo : hi);
+                    if constexpr (!TWICE)
+                        p_lo[b][t][h] = transpose8(lo);
                 }
         }
         const int vr = (lane & 7) + (lane >> 4) * 8, vc = (lane >> 3) & 1;
@@ -290,14 +312,23 @@ struct Acc<C, true> {
                 uint32_t a0, a1, a2, a3;
                 ldsm4t(vs + C::at(b * 16 + vr, k * 2 + vc), a0, a1, a2, a3);
 #pragma unroll
-                for (int t = 0; t < NT; t++)
+                for (int t = 0; t < NT; t++) {
                     mma16816(o[k][t], a0, a1, a2, a3, p[b][t][0], p[b][t][1]);
+                    if constexpr (!TWICE)
+                        mma16816(o[k][t], a0, a1, a2, a3, p_lo[b][t][0], p_lo[b][t][1]);
+                }
             }
         }
     }
 
-    // Sums over the lanes' keys.
+    // Sums over the lanes' keys, and over P's two halves where they have columns of their own.
     __device__ __forceinline__ void finish() {
+        if constexpr (TWICE)
+#pragma unroll
+            for (int k = 0; k < KS; k++)
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    o[k][0][c] += __shfl_xor_sync(0xffffffffu, o[k][0][c], 2);
 #pragma unroll
         for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -979,7 +1010,9 @@ int launch_rows(const AttnParams &p, int B, unsigned flags, cudaStream_t s) {
 template <typename T, int DP>
 int launch_dp(const AttnParams &p, int B, unsigned flags, cudaStream_t s) {
     if constexpr (std::is_same<T, half>::value)
-        return p.rows > 8 ? launch_rows<T, DP, 16>(p, B, flags, s) : launch_rows<T, DP, 8>(p, B, flags, s);
+        return p.rows > 8   ? launch_rows<T, DP, 16>(p, B, flags, s)
+               : p.rows > 4 ? launch_rows<T, DP, 8>(p, B, flags, s)
+                            : launch_rows<T, DP, 4>(p, B, flags, s);
     else
         return p.rows > 4   ? launch_rows<T, DP, 8>(p, B, flags, s)
                : p.rows > 2 ? launch_rows<T, DP, 4>(p, B, flags, s)
