@@ -447,7 +447,7 @@ struct Acc<C, false> {
         }
 #pragma unroll
         for (int r = 0; r < C::ROWS; r++) {
-            s[r] = m[r] == -INFINITY ? 0.0f : ex2(s[r] - m[r]);
+            s[r] = ex2(s[r] - (m[r] == -INFINITY ? 0.0f : m[r]));   // NaN stays NaN, whatever m is
             l[r] += s[r];   // this lane's key; the eight keys are added in finish()
         }
         const int col = lane % LPR, sub = lane / LPR;

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from tests.paged_util import attn_ref, paged_case
+from tests.paged_util import attn_ref, attn_tolerance, paged_case
 from tests.test_gpu_paged import F16, F32, mnb, run_attn  # noqa: F401  (mnb: a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -92,6 +92,28 @@ def clean(case):
         t[live] = rows
     q[~torch.isfinite(q)] = 0
     return q, k, v, table, n
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("i", range(len(SPOILT)))
+@pytest.mark.parametrize("what", ["query", "key", "value"])
+def test_nan_in_a_live_row_is_seen(mnb, cuda_dev, shape, what, i, dtype):  # noqa: F811
+    """A NaN among a head's scores makes its output NaN, one among its values the output's column; the rest is, bit for
+    bit, what it is without.  (Heads that share a KV head decide together when their maxima move: beside a query of NaN
+    the others are within their rounding errors, twice, of what they were.)"""
+    case, hit = spoil(i, dtype, what, float("nan"))
+    out, lse = run_attn(mnb, cuda_dev, case, 0.1)
+    without = clean(case)
+    want, wl = run_attn(mnb, cuda_dev, without, 0.1)
+    gone = hit.all(-1)
+    assert torch.equal(torch.isnan(out), hit)
+    if what != "query":
+        assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~gone], wl[~gone])
+    else:
+        q, lens = without[0], without[4].tolist()
+        t_out, t_lse = attn_tolerance(*attn_ref(*without, 0.1), dtype, max(lens), q.shape[2])
+        assert bool(((out - want).abs().double() <= 2 * t_out)[~hit].all())
+        assert bool(((lse - wl).abs().double() <= 2 * t_lse)[~gone].all())
 
 
 @pytest.mark.parametrize("dtype", [F16, F32])
