@@ -479,10 +479,12 @@ typedef struct mnb_paged_attention_args {
  * Scores, softmax statistics and sums are fp32; with fp16, a probability enters
  * its product with V as two fp16 numbers, which keep 21 bits of it and all that
  * is above 2^-34 of the largest.  n = 0: out = 0, lse = -inf
- * (a batch padded to B requests).  n above max_blocks * page_size counts as
- * that, n below 0 as 0 (status bit 1); keys of a page id outside the pool are
- * left out (bit 0).  Nothing behind a request's n tokens is read: entries of
- * the block table and rows of its last page there may hold anything.
+ * (a batch padded to B requests).  A NaN or +inf among a head's scores makes
+ * out and lse NaN; keys whose score is -inf have no weight.  n above
+ * max_blocks * page_size counts as that, n below 0 as 0 (status bit 1); keys of
+ * a page id outside the pool are left out (bit 0).  Nothing behind a request's n
+ * tokens is read: entries of the block table and rows of its last page there may
+ * hold anything.
  *   lse fp32 [B][Hq] or NULL.  1 <= Hq <= 4096, Hq % Hkv == 0, 0 <= B <= 4096,
  *   max_blocks * page_size <= 2^31 - 64.
  *   Calls of the same sizes on one GPU give the same results, bit for bit.

@@ -166,8 +166,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     return r;
 }
 
-// log sum exp from a maximum in log2 units and a sum relative to it.
-__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? m * kLn2 + logf(l) : -INFINITY; }
+// log sum exp from a maximum in log2 units and a sum relative to it (0: no key; NaN where a score was NaN).
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : m * kLn2 + logf(l); }
 
 // The running softmax of one segment in a warp's registers.  The maximum m is a
 // reference, not the exact maximum: it moves, and o and l are rescaled, only
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(C::kWarpsMost * 32) paged_attention_kernel(con
         const int head = head_of(r);
         if (head < 0)
             return;
-        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         if (c < p.D) {
             T *d = (T *)p.out + b * p.o_bs + head * p.o_hs + c;
             store2(d, o.x * inv, o.y * inv);

@@ -118,6 +118,19 @@ def test_nan_in_a_live_row_is_seen(mnb, cuda_dev, shape, what, i, dtype):  # noq
 
 @pytest.mark.parametrize("dtype", [F16, F32])
 @pytest.mark.parametrize("i", range(len(SPOILT)))
+@pytest.mark.parametrize("what,value", [("query", float("nan")), ("key", float("nan")), ("key", float("inf"))])
+def test_lse_of_scores_without_a_sum(mnb, cuda_dev, shape, what, value, i, dtype):  # noqa: F811
+    """Where a score is NaN or +inf there is no sum of exponentials: lse and out are NaN, not the -inf and zeros of a
+    request without keys."""
+    case, hit = spoil(i, dtype, what, value)
+    case[0][..., case[0].shape[2] // 2 + 1].abs_().add_(1.0)     # times infinity: +inf
+    out, lse = run_attn(mnb, cuda_dev, case, 0.1)
+    assert torch.equal(torch.isnan(lse), hit.all(-1)) and torch.equal(torch.isnan(out), hit)
+    assert bool(torch.isfinite(lse[~hit.all(-1)]).all())
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("i", range(len(SPOILT)))
 @pytest.mark.parametrize("value", [float("inf"), float("-inf")])
 def test_infinite_value_in_a_live_row(mnb, cuda_dev, shape, value, i, dtype):
     """p times infinity, p > 0, is infinite: the output's column has it, no other place is touched."""
