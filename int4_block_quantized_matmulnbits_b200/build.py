@@ -32,7 +32,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills", "-I", os.path.join(ROOT, "include")]
 SOURCES = ["api.cu", "quantize.cu", "gemv.cu", "gemv_tc.cu", "gemv_resident.cu", "gemv_chain.cu", "gemm_tcgen05.cu", "embed.cu", "gptq.cu",
            "paged.cu", "paged_attention.cu"]
-HEADERS = ["common.cuh", "internal.h"]
+HEADERS = ["common.cuh", "internal.h", "raise_limit.h"]
 
 
 def _stale(target, deps):

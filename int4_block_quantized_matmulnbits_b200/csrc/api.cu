@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "raise_limit.h"
 
 namespace mnb {
 
@@ -66,12 +67,9 @@ cudaError_t ensure_dynamic_smem(const void *kernel, int bytes, int *cache) {
         return e;
     if (dev < 0 || dev >= kMaxDevices)
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (bytes <= cache[dev])
-        return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        cache[dev] = bytes;   // two threads racing here both set the same attribute
-    return e;
+    return (cudaError_t)raise_limit(&cache[dev], bytes, [&](int n) {
+        return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+    });
 }
 
 // Limits: sizes fit comfortably in 32-bit element indices of one row and in

@@ -32,7 +32,7 @@ int device_sm_count();
 // Raises a kernel's dynamic shared-memory limit to `bytes` on the current
 // device when it is below that; `cache` (one entry per device, zero-initialized
 // by the caller as a static array of kMaxDevices) remembers what each device
-// was given.  Returns a cudaError_t.
+// was given.  Threads may ask for different sizes at once.  Returns a cudaError_t.
 constexpr int kMaxDevices = 128;
 cudaError_t ensure_dynamic_smem(const void *kernel, int bytes, int *cache);
 
