@@ -158,20 +158,32 @@ class PagedCache:
         self.q = torch.zeros((requests, Hq, D), dtype=dtype, device=device)
         self.ws = torch.zeros((mnb_paged_attention_workspace_bytes(requests, Hq, Hkv, D, dtype),), dtype=torch.uint8,
                               device=device)
+        self._own_slots = self._decode = False   # of the step that begin() has begun: see there
 
     launches_per_step = 1            # begin(); end() is two copies
     launches_per_layer = 2
 
     def begin(self, new=None, slots=None, positions=None, flags=0, stream=None):
         """Pages and slots of new [requests] more tokens a request (None: one each, a decode step), the slots and
-        positions of the new tokens in buffers of the caller's then."""
-        slots, positions = (self.slots, self.positions) if slots is None else (slots, positions)
+        positions of the new tokens in buffers of the caller's then.  The new tokens stand one request behind the
+        other: with a request that gets none or several, row b is not request b's, so layer() takes decode steps only,
+        and append() without slots only steps whose slots are in the cache's own buffers."""
+        if (slots is None) != (positions is None):
+            raise ValueError("slots and positions go together")
+        self._own_slots = self._decode = False
+        own, decode = slots is None, new is None and slots is None
+        slots, positions = (self.slots, self.positions) if own else (slots, positions)
         mnb_paged_tables(self.lens, self.one if new is None else new, self.table, self.page_size, self.pages,
                          self.free, self.start, self.new_lens, self.cu_new, slots, positions, self.next, self.status,
                          flags, stream)
+        self._own_slots, self._decode = own, decode
 
     def append(self, layer, q, k, v, q_out, slots=None, positions=None, flags=0, stream=None):
         """q [T, Hq, D] normed and rotated into q_out, k and v [T, Hkv, D] into the layer's pools."""
+        if (slots is None) != (positions is None):
+            raise ValueError("slots and positions go together")
+        if slots is None and not self._own_slots:
+            raise RuntimeError("append() without slots: begin() has put none into the cache's own buffers")
         slots, positions = (self.slots, self.positions) if slots is None else (slots, positions)
         qw, kw = (None, None) if self.norms is None else self.norms[layer]
         mnb_rope_append(q, k, v, self.k[layer], self.v[layer], slots, positions, self.cos, self.sin, q_out, qw, kw,
@@ -179,6 +191,8 @@ class PagedCache:
 
     def layer(self, layer, q, k, v, out, flags=0, stream=None):
         """One layer of a decode step: out [requests, Hq, D] from this step's q, k and v."""
+        if not self._decode:
+            raise RuntimeError("layer() outside a decode step: it follows begin() without new tokens or slots given")
         self.append(layer, q, k, v, self.q, flags=flags, stream=stream)
         mnb_paged_attention(self.q, self.k[layer], self.v[layer], self.table, self.new_lens, self.scale, out, self.ws,
                             None, self.status, flags, stream)
@@ -190,6 +204,7 @@ class PagedCache:
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             self.lens.copy_(self.new_lens)
             self.start.copy_(self.next)
+        self._own_slots = self._decode = False
 
     def state(self):
         """Lengths, free-list position and status, to be given to restore(): steps in between are then undone (their
