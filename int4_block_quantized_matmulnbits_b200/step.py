@@ -121,6 +121,14 @@ def fuse_decoder(linears, swiglu=False):
     return out
 
 
+def _on(stream):
+    """A context in which torch works on `stream`: None (the current one), a Stream, or a handle as the library's calls
+    take it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
 class PagedCache:
     """Keys and values of a decoder's layers in pages, for up to `requests` requests at once.
 
@@ -131,7 +139,9 @@ class PagedCache:
     (mnb_paged_attention), end() makes the new lengths current.  All layers share the
     table; each has a pool of its own, [pages, page_size, Hkv, D].
 
-    cos, sin: fp32 [max_len, rot_dim / 2] (None: no rotation).  norms: per layer a pair
+    max_len: the tokens that a request may hold; a step that would give it more is
+    refused for that request (status 2) and leaves it as it is.  cos, sin: fp32
+    [max_len or more, rot_dim / 2] (None: no rotation).  norms: per layer a pair
     of fp32 [D] RMS-norm weights of q and k, or None.  status: the device word that the
     three calls report to; check() reads it.
     """
@@ -142,6 +152,12 @@ class PagedCache:
         self.page_size, self.cos, self.sin, self.norms, self.eps = page_size, cos, sin, norms, eps
         self.scale = D ** -0.5 if scale is None else scale
         blocks = -(-max_len // page_size)
+        self.max_len, self._room = max_len, blocks * page_size
+        if (cos is None) != (sin is None):
+            raise ValueError("cos and sin go together")
+        for name, t in (("cos", cos), ("sin", sin)):
+            if t is not None and t.shape[0] < max_len:   # positions without an angle would be dropped
+                raise ValueError(f"{name} has {t.shape[0]} rows for max_len = {max_len}")
         self.pages = requests * blocks if pages is None else pages
         self.k, self.v = ([torch.zeros((self.pages, page_size, Hkv, D), dtype=dtype, device=device)
                            for _ in range(layers)] for _ in range(2))
@@ -173,9 +189,18 @@ class PagedCache:
         self._own_slots = self._decode = False
         own, decode = slots is None, new is None and slots is None
         slots, positions = (self.slots, self.positions) if own else (slots, positions)
-        mnb_paged_tables(self.lens, self.one if new is None else new, self.table, self.page_size, self.pages,
-                         self.free, self.start, self.new_lens, self.cu_new, slots, positions, self.next, self.status,
-                         flags, stream)
+        lens, new, over = self.lens, self.one if new is None else new, None
+        if self.max_len < self._room:
+            # The tables know whole pages only: requests that would pass max_len inside their last page are shown to
+            # them as full (five small launches of torch's for a max_len that is no multiple of page_size).
+            with _on(stream):
+                over = lens.long() + new > self.max_len
+                lens = lens.masked_fill(over, self._room)
+        mnb_paged_tables(lens, new, self.table, self.page_size, self.pages, self.free, self.start, self.new_lens,
+                         self.cu_new, slots, positions, self.next, self.status, flags, stream)
+        if over is not None:
+            with _on(stream):
+                self.new_lens.copy_(torch.where(over, self.lens, self.new_lens))
         self._own_slots, self._decode = own, decode
 
     def append(self, layer, q, k, v, q_out, slots=None, positions=None, flags=0, stream=None):
@@ -199,9 +224,7 @@ class PagedCache:
 
     def end(self, stream=None):
         """The step's lengths and free-list position become current."""
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream))   # a handle, as the library's calls take it
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with _on(stream):
             self.lens.copy_(self.new_lens)
             self.start.copy_(self.next)
         self._own_slots = self._decode = False

@@ -1,0 +1,54 @@
+"""step.PagedCache at the end of its room and on other streams than the current one."""
+import pytest
+import torch
+
+from int4_block_quantized_matmulnbits_b200 import step
+from tests.paged_util import attn_ref
+
+pytestmark = pytest.mark.gpu
+F16 = torch.float16
+
+
+@pytest.mark.parametrize("rotate", [True, False])
+def test_cache_whose_max_len_is_inside_a_page(cuda_dev, rotate):
+    """Room for 30 tokens in pages of 16: 30 steps are granted and attended over, captured ones among them; the next is
+    refused as a length without room and leaves the request and its rows as they are."""
+    gen = torch.Generator().manual_seed(30)
+    ang = torch.rand(30, 32, generator=gen) * 6
+    c = step.PagedCache(1, 1, 2, 1, 64, max_len=30, page_size=16, device=cuda_dev,
+                        **(dict(cos=ang.cos().to(cuda_dev), sin=ang.sin().to(cuda_dev)) if rotate else {}))
+    q, k, v = (torch.empty(1, h, 64, dtype=F16, device=cuda_dev) for h in (2, 1, 1))
+    out = torch.empty(1, 2, 64, dtype=F16, device=cuda_dev)
+
+    def one():
+        c.begin()
+        c.layer(0, q, k, v, out)
+        c.end()
+
+    def check_out(n):
+        assert c.lens.tolist() == [n]
+        ref, _, spread, _ = attn_ref(c.q.cpu(), c.k[0].cpu(), c.v[0].cpu(), c.table.cpu(), [n], c.scale)
+        # 2^-11 for the output; 2^-15 of the magnitudes is far more than 30 keys' fp32 sums can lose
+        assert bool(((out.cpu().double() - ref).abs() <= 2.0 ** -11 * ref.abs() + 2.0 ** -15 * spread + 2.0 ** -25).all())
+
+    g = None
+    for i in range(30):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=gen))
+        if i < 10:
+            one()
+            continue
+        if g is None:
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                one()
+        g.replay()
+    c.check()
+    check_out(30)
+    rows = c.k[0].clone()
+    for again in (g.replay, one):
+        again()
+        assert c.lens.tolist() == [30] and torch.equal(c.k[0], rows)
+        with pytest.raises(RuntimeError, match="status 2"):
+            c.check()

@@ -74,3 +74,35 @@ def test_a_begin_that_fails_begins_no_step(calls, monkeypatch):
         c.begin()
     with pytest.raises(RuntimeError, match="decode step"):
         c.layer(0, *rows(), torch.zeros(3, 2, 64, dtype=torch.float16))
+
+
+def test_max_len_inside_a_page(monkeypatch):
+    """max_len = 30 in pages of 16, whose tables have room for 32: a request that would hold 31 is shown to them as
+    full, so that they refuse it, and keeps its length; the others are not touched."""
+    c, seen = cache(max_len=30, page_size=16), []
+
+    def tables(lens, new, *a):      # as the library does it, but for pages and slots
+        seen.append(lens.tolist())
+        a[5].copy_(torch.where(lens.long() + new > 32, lens, lens + new))
+
+    monkeypatch.setattr(step, "mnb_paged_tables", tables)
+    c.lens.copy_(torch.tensor([29, 30, 7]))
+    c.begin()
+    assert seen == [[29, 32, 7]] and c.new_lens.tolist() == [30, 30, 8] and c.lens.tolist() == [29, 30, 7]
+    c.begin(torch.tensor([2, 0, 2 ** 31 - 1], dtype=torch.int32), c.slots, c.positions)
+    assert seen[1] == [32, 30, 32] and c.new_lens.tolist() == [29, 30, 7]
+    whole = cache(max_len=32, page_size=16)      # nothing to hide here
+    whole.lens.fill_(31)
+    whole.begin()
+    assert seen[2] == [31, 31, 31]
+
+
+def test_every_position_has_an_angle():
+    """Without, the append would drop keys while the lengths go on."""
+    angles = torch.zeros(30, 32)
+    assert cache(max_len=30, cos=angles, sin=angles).max_len == 30
+    for kw in (dict(cos=angles[:29], sin=angles[:29]), dict(cos=angles, sin=angles[:29])):
+        with pytest.raises(ValueError, match="29 rows for max_len = 30"):
+            cache(max_len=30, **kw)
+    with pytest.raises(ValueError, match="go together"):
+        cache(max_len=30, cos=angles)
