@@ -229,20 +229,28 @@ class PagedCache:
             self.start.copy_(self.next)
         self._own_slots = self._decode = False
 
-    def state(self):
+    def state(self, stream=None):
         """Lengths, free-list position and status, to be given to restore(): steps in between are then undone (their
-        pages go back to the list; the rows they wrote are written again by the next steps)."""
-        return [t.clone() for t in (self.lens, self.start, self.status)]
+        pages go back to the list; the rows they wrote are written again by the next steps).  Both in order with the
+        steps of `stream`."""
+        with _on(stream):
+            return [t.clone() for t in (self.lens, self.start, self.status)]
 
-    def restore(self, state):
-        for t, was in zip((self.lens, self.start, self.status), state):
-            t.copy_(was)
+    def restore(self, state, stream=None):
+        with _on(stream):
+            for t, was in zip((self.lens, self.start, self.status), state):
+                t.copy_(was)
 
-    def check(self):
-        """Raises if a step since the last check met a bad index, a request without room or an empty free list
-        (synchronizes)."""
-        word = int(self.status.item())
-        self.status.zero_()
+    def check(self, stream=None):
+        """Raises if a step since the last check met a bad index, a request without room or an empty free list.
+        Waits for the steps of `stream` (None: for the whole device, on whichever streams they run)."""
+        if stream is None and self.status.is_cuda:
+            torch.cuda.synchronize(self.status.device)
+        with _on(stream):
+            word = int(self.status.item())
+            self.status.zero_()
+        if stream is None and self.status.is_cuda:
+            torch.cuda.synchronize(self.status.device)   # cleared before a later step on another stream reports
         if word:
             raise RuntimeError(f"paged cache: status {word} (1 a bad index, 2 a length without room, 4 no free page)")
 

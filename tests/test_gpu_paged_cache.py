@@ -52,3 +52,42 @@ def test_cache_whose_max_len_is_inside_a_page(cuda_dev, rotate):
         assert c.lens.tolist() == [30] and torch.equal(c.k[0], rows)
         with pytest.raises(RuntimeError, match="status 2"):
             c.check()
+
+
+def full_step(cache, stream, busy):
+    """A step on `stream` that a full cache refuses, behind some milliseconds of other work there."""
+    x = torch.zeros(1, 2, 64, dtype=F16, device=cache.lens.device)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for _ in range(20):
+            busy @ busy
+    cache.begin(stream=stream)
+    cache.layer(0, x, x[:, :1], x[:, :1], x, stream=stream)
+    cache.end(stream)
+
+
+@pytest.mark.parametrize("how", ["stream", "handle", "none"])
+def test_check_waits_for_the_steps_stream(cuda_dev, how):
+    """A refused step on a side stream, still running when check() is called: check() sees it, once."""
+    c = step.PagedCache(1, 1, 2, 1, 64, max_len=16, page_size=16, device=cuda_dev)
+    c.lens.fill_(16)
+    busy, s = torch.zeros(4096, 4096, device=cuda_dev), torch.cuda.Stream()
+    given = dict(stream=[s], handle=[s.cuda_stream], none=[])[how]
+    for _ in range(2):
+        full_step(c, s, busy)
+        with pytest.raises(RuntimeError, match="status 2"):
+            c.check(*given)
+        c.check(*given)
+
+
+def test_state_and_restore_on_the_steps_stream(cuda_dev):
+    """state() behind a step that is still running holds its lengths, restore() undoes what follows it."""
+    c = step.PagedCache(1, 1, 2, 1, 64, max_len=64, page_size=16, device=cuda_dev)
+    busy, s = torch.zeros(4096, 4096, device=cuda_dev), torch.cuda.Stream()
+    full_step(c, s, busy)
+    was = c.state(s)
+    full_step(c, s, busy)
+    c.restore(was, s)
+    s.synchronize()
+    assert c.lens.tolist() == [1] and was[0].tolist() == [1] and int(c.start) == 1
+    c.check(s)
