@@ -1,8 +1,8 @@
 """MatMulNBits (weight-only int4, block-quantized) for NVIDIA B200 -- Python binding.
 
 A thin layer over ``libmnb.so`` (the sm_100a kernels and their C ABI, declared in
-``include/mnb.h``): ctypes, and ``_binding.so`` for the paged cache's calls.  Every function here has the name of the C
-entry point it calls and only marshals arguments: torch tensors become device
+``include/mnb.h``): ctypes, and the C++ module ``_binding`` for the paged cache's
+calls.  Every function here has the name of the C entry point it calls and only marshals arguments: torch tensors become device
 pointers, dtypes become ``mnb_dtype`` values, the stream defaults to torch's
 current stream.  All arithmetic runs in the CUDA kernels; there is no CPU path.
 If the library cannot be loaded, importing this package raises.
@@ -57,7 +57,7 @@ def _load():
     # a no-op otherwise.  Raises if nvcc fails: there is no fallback path.
     from . import build as _build
 
-    _build.build()
+    _build.build(binding=False)
     lib = ctypes.CDLL(lib_path)
     i64, i32, u32, vp, sz = ctypes.c_int64, ctypes.c_int, ctypes.c_uint, ctypes.c_void_p, ctypes.c_size_t
     P = ctypes.POINTER
@@ -308,7 +308,35 @@ def mnb_gptq_quantize(W, U, dead, bs, has_zp, packed, scales, zp, stream=None):
 # layer: _binding (csrc/binding.cpp) reads and checks the tensors and makes the C
 # call; what a failed check has found is worked out afterwards, in _explain.
 
-from . import _binding  # noqa: E402  (built and loaded with libmnb.so)
+
+class _NoBinding:
+    """In the place of a _binding that cannot be built or loaded: the paged cache's calls raise, the others, which need
+    none of it, run."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        if name.startswith("__"):
+            raise AttributeError(name)
+        raise ImportError(f"the paged cache's calls need csrc/binding.cpp, built for this Python and torch: {self._why}")
+
+
+def _load_binding():
+    from . import build as _build
+
+    try:
+        _build.build_binding()
+        from . import _binding
+
+        if _binding.torch_version != str(torch.__version__):
+            raise ImportError(f"built for torch {_binding.torch_version}, this is {torch.__version__}")
+        return _binding
+    except Exception as e:  # no compiler, no headers, another Python or torch: told where a call needs it
+        return _NoBinding(f"{type(e).__name__}: {e}")
+
+
+_binding = _load_binding()
 
 _PAGED_DT = {torch.float16: MNB_F16, torch.float32: MNB_F32}
 

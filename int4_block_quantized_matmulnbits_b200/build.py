@@ -9,13 +9,16 @@ Each .cu file compiles to an object under _build/, then one shared library is
 linked next to this file.  CUDA runtime is linked statically, so the library
 only needs the NVIDIA driver at run time.
 
-_binding.so, linked next to it with g++, is the Python module that makes the
-paged cache's calls (csrc/binding.cpp); it needs the torch it was built with.
+The _binding module, linked next to it with g++, makes the paged cache's calls for
+Python (csrc/binding.cpp).  It needs the Python and the torch that it was built
+for, so its name carries the one (_binding.<tag>.so) and it checks the other; the
+rest of the library needs neither.
 """
 from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -48,28 +51,42 @@ DEBUG_SOURCES = ["gemv_resident.cu"]
 DEBUG_OUT = os.path.join(HERE, "libmnb_debug.so")
 
 
-BINDING = os.path.join(HERE, "_binding.so")
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def torch_version(root):
+    """__version__ of the torch in the folder `root`, without importing it."""
+    with open(os.path.join(root, "version.py")) as f:
+        return re.search(r"^__version__[^=]*= *['\"]([^'\"]+)['\"]", f.read(), re.M).group(1)
 
 
 def build_binding(verbose: bool = False) -> str:
-    """_binding.so (csrc/binding.cpp): the paged cache's calls for Python, against torch's headers and libmnb.so."""
+    """The _binding module (csrc/binding.cpp): the paged cache's calls for Python, against torch's headers and libmnb.so."""
     src, torch = os.path.join(CSRC, "binding.cpp"), os.path.dirname(importlib.util.find_spec("torch").origin)
-    if _stale(BINDING, [src, os.path.join(ROOT, "include", "mnb.h"), os.path.join(torch, "version.py")]):
+    version = torch_version(torch)
+    stamp = os.path.join(BUILD, "binding.torch")   # the torch that it was built for
+    same = os.path.exists(stamp) and open(stamp).read() == version
+    if not same or _stale(BINDING, [src, os.path.join(ROOT, "include", "mnb.h")]):
         inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
-               "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
-               "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
-               "-I", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), src, "-o", BINDING + ".tmp",
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-Wextra",
+               f'-DMNB_TORCH="{version}"', "-I", os.path.join(ROOT, "include"), "-isystem", sysconfig.get_paths()["include"],
+               "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+               "-isystem", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), src, "-o", BINDING + ".tmp",
                "-L", HERE, "-l:libmnb.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
                "-ltorch_python"]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(BINDING + ".tmp", BINDING)
+        with open(stamp, "w") as f:
+            f.write(version)
+        old = os.path.join(HERE, "_binding.so")   # a name that any Python would load
+        if os.path.exists(old):
+            os.remove(old)
     return BINDING
 
 
-def build(verbose: bool = False, ptxas_verbose: bool = False, debug: bool = False) -> str:
+def build(verbose: bool = False, ptxas_verbose: bool = False, debug: bool = False, binding: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", f) for f in ("mnb.h", "mnb_tune.h")]
     objs = []
@@ -93,7 +110,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, debug: bool = Fals
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, out)
-    if not debug:
+    if binding and not debug:
         build_binding(verbose)
     return out
 
