@@ -485,8 +485,8 @@ typedef struct mnb_paged_attention_args {
  * a page id outside the pool are left out (bit 0).  Nothing behind a request's n
  * tokens is read: entries of the block table and rows of its last page there may
  * hold anything.
- *   lse fp32 [B][Hq] or NULL.  1 <= Hq <= 4096, Hq % Hkv == 0, 0 <= B <= 4096,
- *   max_blocks * page_size <= 2^31 - 64.
+ *   lse fp32 [B][Hq] or NULL.  |scale| <= 2e38, 1 <= Hq <= 4096, Hq % Hkv == 0,
+ *   0 <= B <= 4096, max_blocks * page_size <= 2^31 - 64.
  *   Calls of the same sizes on one GPU give the same results, bit for bit.
  *   The launch shape follows B, the heads and max_blocks (the lengths are on the
  *   device): a table much wider than the longest request needs costs time; a

@@ -647,8 +647,8 @@ int mnb_paged_attention(const mnb_paged_attention_args *args, unsigned flags, vo
         table_stride > kMaxStride)
         return fail(MNB_ERR_SHAPE, "%s: block table of %lld columns, row stride %lld", fn, (long long)max_blocks,
                     (long long)table_stride);
-    if (!(scale >= -3.0e38f && scale <= 3.0e38f))
-        return fail(MNB_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+    if (!(scale >= -2.0e38f && scale <= 2.0e38f))   // times log2 e, as the kernel takes it, it has to be finite
+        return fail(MNB_ERR_INVALID_ARG, "%s: scale is not a number of at most 2e38", fn);
     if (flags & ~(unsigned)MNB_FLAG_PDL)
         return fail(MNB_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
     if (B == 0)
