@@ -17,13 +17,13 @@ def shape(mnb, request):  # noqa: F811
     mnb._lib.mnb_tune_paged_attention(0, 0, 0)
 
 
-def two_keys(n, at, G, D, ps, seed):
+def two_keys(n, at, G, D, ps, seed, dtype):
     """G query heads on one KV head, q_i = a_i e_0, and n keys of which two count: scores 0 and -a_i, all others below
     -6000 (weight 0 exactly).  Their values are c and -c e^a for columns of heads' own a: the output of head i is nearly
     nothing in the columns d % G == i, so what its probabilities lose shows there."""
     gen = torch.Generator().manual_seed(seed)
-    q, k, v, table, lens = paged_case(seed, [n], G, 1, D, ps, F16)
-    a = (0.1 + 3.5 * torch.rand(G, generator=gen)).to(F16)
+    q, k, v, table, lens = paged_case(seed, [n], G, 1, D, ps, dtype)
+    a = (0.1 + 3.5 * torch.rand(G, generator=gen)).to(dtype)
     q.zero_()
     q[0, :, 0] = a
     j = torch.arange(n)
@@ -32,7 +32,7 @@ def two_keys(n, at, G, D, ps, seed):
     c = 0.05 * (1 + torch.rand(D, generator=gen, dtype=torch.float64))
     for key, score, val in ((at[0], 0.0, c), (at[1], -1.0, -c * torch.exp(a.double()).repeat(D // G))):
         k[page[key], off[key], 0, 0] = score
-        v[page[key], off[key], 0] = val.to(F16)
+        v[page[key], off[key], 0] = val.to(dtype)
     return (q, k, v, table, lens), a
 
 
@@ -40,16 +40,27 @@ def two_keys(n, at, G, D, ps, seed):
                                   (9000, (4100, 4107))])
 @pytest.mark.parametrize("G,D", [(1, 64), (2, 128), (4, 80), (8, 128), (8, 256), (16, 64)])
 def test_fp16_probabilities_keep_fp32s_bits(mnb, cuda_dev, shape, G, D, n, at):  # noqa: F811
+    check_two_keys(mnb, cuda_dev, n, at, G, D, F16)
+
+
+@pytest.mark.parametrize("G,D", [(1, 64), (4, 128), (8, 256)])
+def test_fp32_probabilities_of_a_long_request(mnb, cuda_dev, shape, G, D):  # noqa: F811
+    """However long the request, keys without weight add zeros exactly: the bound does not grow with it."""
+    check_two_keys(mnb, cuda_dev, 9000, (4100, 4107), G, D, F32)
+
+
+def check_two_keys(mnb, cuda_dev, n, at, G, D, dtype):  # noqa: F811
     """|out - ref| from the arithmetic: the scores' products and sums are exact (one product is not zero); scaling by
     log2 e, the product and the difference to the maximum: three roundings of at most a log2 e + 16; 2^-22 for the
     exponential; a probability as two fp16 numbers: 2^-21 of it; at most 16 sums of terms that are not zero at 2^-23 each;
     the quotient 2^-23.  All of it times the sum of magnitudes: (3 (1.45 a + 16) 2^-24 + 2^-22 + 2^-21 + 17 2^-23) of it,
     below (1.1 a + 24) 2^-22.  Then the output's own rounding."""
-    (q, k, v, table, lens), a = two_keys(n, at, G, D, 16, n + D)
+    (q, k, v, table, lens), a = two_keys(n, at, G, D, 16, n + D, dtype)
     case = (q, k, v, table, lens)
     out, lse = run_attn(mnb, cuda_dev, case, 1.0)
     ref, rl, spread, _ = attn_ref(*case, 1.0)
-    bound = 2.0 ** -11 * ref.abs() + ((1.1 * a.double() + 24) * 2.0 ** -22)[None, :, None] * spread + 2.0 ** -25
+    u, least = (2.0 ** -11, 2.0 ** -25) if dtype == F16 else (2.0 ** -24, 0.0)
+    bound = u * ref.abs() + ((1.1 * a.double() + 24) * 2.0 ** -22)[None, :, None] * spread + least
     d = (out.double() - ref).abs()
     assert bool((d <= bound).all()), f"off by {float((d / spread).max()):.3g} of the sum of magnitudes"
     assert float((lse.double() - rl).abs().max()) <= 5 * 2.0 ** -22 * 4
