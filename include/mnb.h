@@ -444,7 +444,8 @@ typedef struct mnb_rope_append_args {
  * (fp32 [num_pos][rot_dim / 2]) and x a head of q or k:
  *   x <- x * w / sqrt(mean(x^2) + eps)          when q_weight / k_weight (fp32 [D]) is given,
  *   (x_i, x_{i+R/2}) <- (x_i c_i - x_{i+R/2} s_i, x_{i+R/2} c_i + x_i s_i),  i < R/2, R = rot_dim,
- * all in fp32, rounded once; q goes to q_out (which may be q itself), k and v
+ * all in fp32, rounded once; q goes to q_out (which may be q itself, and shares
+ * no memory with q, k or v otherwise), k and v
  * (v as it is) to slot slots[t] of the cache.  rot_dim is a multiple of 8, at
  * most D; 0 = no rotation (positions, cos and sin are then not read).  Hq = 0:
  * no q.  Strides are in elements, multiples of 16 bytes; q, k and v may be

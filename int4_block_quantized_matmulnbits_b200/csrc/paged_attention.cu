@@ -24,8 +24,8 @@
 // CTA barrier, and a warp waits for its own copies only.
 //
 // Bound by the cache's bytes where there are many (64 requests of up to 8192 tokens
-// in 8 heads of 128: 164 us, 6650 GB/s), by latency where there are few (one request
-// of 390 tokens: 5.8 us).  A tile is one warp's alone because its chain of products
+// in 8 heads of 128: 162 to 166 us in a graph, 6600 GB/s; 173 us as calls from
+// Python), by latency where there are few (one request of 390 tokens: 5.9 us).  A tile is one warp's alone because its chain of products
 // and exponentials, about 0.65 us, is what a warp's rate is made of: more warps hide
 // it, more copies in flight do not.
 #include <type_traits>
@@ -936,9 +936,15 @@ int launch_cfg(AttnParams p, int B, unsigned flags, cudaStream_t s) {
             split = S, warps = W;
     }
     // More segments than that, or long work for each warp: CTAs of a third of an SM,
-    // about 32 tiles a warp, in turn (64 requests of up to 8192: 167 us as 4 x 4,
-    // 179 as 1 x 4); short segments as CTAs of two warps (256 requests of 100: 27.8
-    // us as 1 x 2, 32 as 1 x 4).
+    // about 32 tiles a warp, in turn (64 requests of up to 8192: 164 us as 4 x 4,
+    // 176 as 1 x 4); short segments as CTAs of two warps (256 requests of 100: 27.8
+    // us as 1 x 2, 32 as 1 x 4).  The lengths are on the device, and no edge between
+    // two and four warps is right for all: even lengths gain from two at any length,
+    // ragged ones from four behind about 24 tiles (40 requests in 16 heads of 64, as
+    // 1 x 2 and 1 x 4: of 1000 tokens 31.5 and 36.1 us, of up to 1000 25.6 and 21.5;
+    // of 1500 45.8 and 51.2, of up to 1500 34.9 and 25.1; of 1600 48.0 and 54.0, of up
+    // to 1600 36.6 and 27.5; 256 requests in 8 heads of 128: of 1000 158 and 156, of up
+    // to 1000 87 and 84).
     if (warps == 0 || (split < kMaxSplit && tiles > 32 * split * warps) || (warps < 3 && tiles > 24 * warps)) {
         const int W = tiles <= 48 ? 2 : most == kMaxWarps ? 4 : 3, long_split = (tiles - 1) / (32 * W) + 1;
         split = long_split > split ? long_split : split;

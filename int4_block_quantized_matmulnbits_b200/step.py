@@ -144,6 +144,9 @@ class PagedCache:
     [max_len or more, rot_dim / 2] (None: no rotation).  norms: per layer a pair
     of fp32 [D] RMS-norm weights of q and k, or None.  status: the device word that the
     three calls report to; check() reads it.
+
+    A row's pages are not handed back while the others go on: restore() of the state
+    that state() gave before the first step makes all rows and pages free again.
     """
 
     def __init__(self, layers, requests, Hq, Hkv, D, max_len, page_size=16, pages=None, dtype=torch.float16,

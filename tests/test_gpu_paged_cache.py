@@ -91,3 +91,25 @@ def test_state_and_restore_on_the_steps_stream(cuda_dev):
     s.synchronize()
     assert c.lens.tolist() == [1] and was[0].tolist() == [1] and int(c.start) == 1
     c.check(s)
+
+
+def test_restore_of_the_empty_state_frees_all(cuda_dev):
+    """A cache with pages for one batch only serves the next after restore(): the same steps, the same bits."""
+    gen = torch.Generator().manual_seed(5)
+    c = step.PagedCache(1, 2, 2, 1, 64, max_len=32, page_size=16, device=cuda_dev)
+    empty = c.state()
+    xs = [[torch.randn(2, h, 64, generator=gen).to(F16).to(cuda_dev) for h in (2, 1, 1)] for _ in range(32)]
+    runs = []
+    for _ in range(2):
+        outs = []
+        for q, k, v in xs:
+            out = torch.empty(2, 2, 64, dtype=F16, device=cuda_dev)
+            c.begin()
+            c.layer(0, q, k, v, out)
+            c.end()
+            outs.append(out)
+        c.check()
+        runs.append(torch.stack(outs))
+        assert int(c.start) == c.pages == 4      # every page is taken
+        c.restore(empty)
+    assert torch.equal(runs[0], runs[1])
