@@ -2,10 +2,12 @@
 
 A thin layer over ``libmnb.so`` (the sm_100a kernels and their C ABI, declared in
 ``include/mnb.h``): ctypes, and the C++ module ``_binding`` for the paged cache's
-calls.  Every function here has the name of the C entry point it calls and only marshals arguments: torch tensors become device
-pointers, dtypes become ``mnb_dtype`` values, the stream defaults to torch's
-current stream.  All arithmetic runs in the CUDA kernels; there is no CPU path.
-If the library cannot be loaded, importing this package raises.
+calls.  Every function here has the name of the C entry point it calls and only
+marshals arguments: torch tensors become device pointers, dtypes become
+``mnb_dtype`` values, the stream defaults to torch's current stream.  All
+arithmetic runs in the CUDA kernels; there is no CPU path.  If the library cannot
+be loaded, importing this package raises; if the C++ module cannot, the paged
+cache's calls do.
 
 Layout (see ``include/mnb.h``): packed uint8 [N, K/2] (element 2j in the low
 nibble of byte j), scales fp32/fp16 [N, K/bs], zero points uint8

@@ -25,9 +25,10 @@
 //
 // Bound by the cache's bytes where there are many (64 requests of up to 8192 tokens
 // in 8 heads of 128: 162 to 166 us in a graph, 6600 GB/s; 173 us as calls from
-// Python), by latency where there are few (one request of 390 tokens: 5.9 us).  A tile is one warp's alone because its chain of products
-// and exponentials, about 0.65 us, is what a warp's rate is made of: more warps hide
-// it, more copies in flight do not.
+// Python), by latency where there are few (one request of 390 tokens: 5.9 us).  A
+// tile is one warp's alone because its chain of products and exponentials, about
+// 0.65 us, is what a warp's rate is made of: more warps hide it, more copies in
+// flight do not.
 #include <type_traits>
 
 #include "common.cuh"
